@@ -96,6 +96,9 @@ typedef struct {
      * at +-448). FP8 caches need dtype = PA_DTYPE_BF16. The pages name FP8
      * only for weights ("vLLM and PagedAttention" §5); an FP8 cache halves the
      * bytes decode reads.
+     * PA_KV_BLOCK_E4M3 or PA_KV_BLOCK_INT8 (2, 3): one-byte codes with a scale for
+     * each block and KV head ("block8" pools, see pa_cache_block8); only the calls
+     * that say so take them, with dtype = PA_DTYPE_BF16.
      */
     int32_t kv_fp8;
     float k_scale; /* > 0 when kv_fp8; ignored otherwise */
@@ -307,6 +310,175 @@ int pa_decode_noalloc(void *out, const void *q, const void *k_cache, const void 
                       const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
                       int32_t num_seqs, int32_t max_context_len, float scale, int32_t partition_tokens,
                       const pa_shape *shape, void *stream);
+
+/*
+ * Rotary positions. The first rot_dim dims of a head are rot_dim / 2 pairs (x, y),
+ * (i, i + rot_dim / 2) in the half layout or (2i, 2i + 1) in the interleaved one. At
+ * position p, pair i turns by a = p * f_i:
+ *   x' = mscale * (x cos a - y sin a),  y' = mscale * (y cos a + x sin a).
+ * Dims from rot_dim on pass through. f_i = base^(-2i / rot_dim), scaled for contexts
+ * longer than the trained one:
+ *   PA_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   PA_ROPE_BASE    base * factor^(rot_dim / (rot_dim - 2)) for base
+ *   PA_ROPE_PARTS   t = (original_len * f_i / 2 pi - low) / (high - low) clamped to
+ *                   [0, 1]: t * f_i + (1 - t) * f_i / factor. Pairs that turn more than
+ *                   `high` times over the original context keep their frequency, those
+ *                   that turn less than `low` times are interpolated.
+ */
+#define PA_ROPE_MAX_DIM 128
+#define PA_ROPE_NONE 0
+#define PA_ROPE_LINEAR 1
+#define PA_ROPE_BASE 2
+#define PA_ROPE_PARTS 3
+
+/* Host memory, filled by pa_rope_init, passed by value to the kernels at each call. */
+typedef struct {
+    int32_t rot_dim;
+    int32_t interleaved;
+    float mscale;
+    int32_t reserved;
+    uint64_t step[PA_ROPE_MAX_DIM / 2]; /* f_i / 2 pi, the turn per position, times 2^64 */
+} pa_rope_plan;
+
+/*
+ * pa_rope_init: fill a plan. rot_dim is a multiple of 16, 16 .. 128 (else
+ * PA_ERR_UNSUPPORTED); base >= 1; factor >= 1 unless scaling is PA_ROPE_NONE; low,
+ * high and original_len count for PA_ROPE_PARTS only (0 <= low < high,
+ * original_len > 0). mscale multiplies cos and sin (1 for none). Host only.
+ */
+int pa_rope_init(pa_rope_plan *plan, int32_t rot_dim, int32_t interleaved, double base, int32_t scaling, double factor,
+                 double low, double high, double original_len, double mscale);
+
+/*
+ * pa_rope: rotate q and k by position.
+ *   q         : rows [H][D] of shape->dtype, token t at q + t * q_stride elements
+ *   k         : rows [Hk][D], token t at k + t * k_stride elements. Strides are at
+ *               least a row and a multiple of 16 bytes, so q and k can be columns of
+ *               one projection's output.
+ *   q_out     : [T][H][D]; k_out : [T][Hk][D]. May be q and k themselves where those
+ *               are contiguous; must not overlap them otherwise.
+ *   positions : int64 [T] device. Angles are exact to 2^-32 of a turn for
+ *               |position| < 2^31 (the turn is kept in 64-bit fixed point).
+ * The rotation is fp32, rounded once. The pool fields of `shape` are checked but not
+ * used. num_tokens == 0 is a no-op.
+ */
+int pa_rope(void *q_out, void *k_out, const void *q, const void *k, int64_t q_stride, int64_t k_stride,
+            const int64_t *positions, int64_t num_tokens, const pa_rope_plan *plan, const pa_shape *shape,
+            void *stream);
+
+/*
+ * pa_rope_and_cache: pa_rope for q and k with pa_reshape_and_cache for the rotated k
+ * and v, in one launch: the new tokens' keys go rotated to their slots.
+ *   q, k, v, strides, positions : as pa_rope (v like k)
+ *   q_out        : [T][H][D]; may be q itself where q is contiguous
+ *   k_cache, v_cache, slot_mapping : as pa_reshape_and_cache. A token with a negative
+ *                  slot is padding: nothing is cached for it; its q_out row is written.
+ * An FP8 pool (kv_fp8 = 1) takes codes of fp32(rotated k) * fp32(1 / k_scale), without a
+ * rounding to bf16 in between.
+ */
+int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                      const int64_t *positions, int64_t num_tokens, const pa_rope_plan *plan, const pa_shape *shape,
+                      void *stream);
+
+/*
+ * block8 pools: one-byte codes [NB][16][Hk][D] with fp32 scales [NB][Hk], for keys and
+ * for values. A cached value is code * scale[block][KV head]. PA_KV_BLOCK_E4M3: FP8
+ * E4M3 codes; PA_KV_BLOCK_INT8: signed integers -127 .. 127. pa_copy_blocks and
+ * pa_swap_blocks move the codes of such pools (as any one-byte pool); the caller moves
+ * the scales' rows.
+ */
+#define PA_KV_BLOCK_E4M3 2
+#define PA_KV_BLOCK_INT8 3
+
+/*
+ * pa_cache_block8: append new tokens to a block8 pool.
+ *   k, v         : bf16 [T][Hk][D]
+ *   k_codes, v_codes, k_scales, v_scales : the pool, updated in place
+ *   slot_mapping : int64 [T], as pa_reshape_and_cache (negative: padding)
+ * A block's rows are filled in order. The tokens of one call that go to one block stand
+ * next to one another in the call; the rows below the lowest of them hold earlier tokens
+ * and keep their values, the rows above are free. For each KV head, s is the least power
+ * of two, 2^-64 .. 2^120, with |x| <= 448 s (E4M3) or 127 s (INT8) for the block's new
+ * elements. With no earlier rows the block's scale becomes s. Otherwise it becomes the
+ * larger of s and what it was, and if it grew the earlier rows are re-coded from
+ * code * old / new. Codes are nearest, ties to even, saturating; infinities saturate and
+ * do not count for s, a NaN becomes E4M3's NaN or INT8's 0.
+ * Two separate groups of tokens for one block in one call, or one slot twice: which
+ * values the block ends with is unspecified. A slot >= NB * 16 is skipped and sets
+ * PA_STATUS_BAD_SLOT. num_tokens == 0 is a no-op.
+ */
+int pa_cache_block8(const void *k, const void *v, void *k_codes, void *v_codes, float *k_scales, float *v_scales,
+                    const int64_t *slot_mapping, int64_t num_tokens, const pa_shape *shape, void *stream);
+
+/* pa_decode_workspace_bytes for pa_decode_block8. */
+int64_t pa_decode_block8_workspace_bytes(int32_t num_seqs, int32_t max_context_len, int32_t partition_tokens,
+                                         const pa_shape *shape);
+
+/*
+ * pa_decode_block8: pa_decode over a block8 pool (bf16 q and out). Arguments as
+ * pa_decode, with the scales ([NB][Hk] each, any finite values >= 0). Scores, softmax
+ * sums and outputs accumulate in fp32; q enters the products as f16 after division by a
+ * power of two for each head, probabilities as f16.
+ */
+int pa_decode_block8(void *out, const void *q, const void *k_codes, const void *v_codes, const float *k_scales,
+                     const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                     const int32_t *context_lens, int32_t num_seqs, int32_t max_context_len, float scale,
+                     int32_t partition_tokens, void *workspace, int64_t workspace_bytes, const pa_shape *shape,
+                     void *stream);
+
+/*
+ * pa_decode_weights: decode that also counts attention weights, for pa_evict.
+ *   out as pa_decode (block8 pools: pa_decode_block8), and for i < context_lens[b]
+ *   weights[b][hk][i] += sum over the query heads h of KV head hk of
+ *                        softmax_i(scale * q[b][h] . K_b[i])
+ *   weights   : fp32 [B][Hk][weights_width], weights_width >= max_context_len. Entries
+ *               past the context are left alone; the caller zeroes a row before its
+ *               sequence's first step (pa_evict leaves the free entries zero).
+ *   k_scales, v_scales : block8 pools' scales; NULL otherwise
+ *   workspace : >= pa_decode_weights_workspace_bytes(...) bytes: pa_decode's, then
+ *               B * H * (max_context_len rounded up to 16) scores and B * H sums, fp32
+ * Each weight is written by one thread, so results repeat bit for bit.
+ */
+int64_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t max_context_len, int32_t partition_tokens,
+                                          const pa_shape *shape);
+int pa_decode_weights(void *out, float *weights, int32_t weights_width, const void *q, const void *k_cache,
+                      const void *v_cache, const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                      int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                      int32_t max_context_len, float scale, int32_t partition_tokens, void *workspace,
+                      int64_t workspace_bytes, const pa_shape *shape, void *stream);
+
+/*
+ * pa_evict: cut every sequence's cache to at most `keep` entries for each KV head.
+ *
+ * Of a context of n > keep entries, KV head hk keeps the first `sinks`, the last
+ * `recent`, and the others of the largest weights[b][hk] (ties to the lower index; NaN
+ * counts as -infinity), `keep` in all; a context of n <= keep keeps everything. Kept
+ * entries go in their order to entries 0, 1, ... of the sequence's new blocks: K and V
+ * rows (block8: re-coded for the new block's scale, the least power of two for its
+ * rows, as in pa_cache_block8) and weights. Heads keep different tokens: after this,
+ * entry i of a sequence is another position for each head, which attention does not
+ * mind once keys are rotated.
+ *   weights       : fp32 [B][Hk][weights_width], weights_width >= max_context_len
+ *   dst_block_tables : int32 [B][dst_blocks_per_seq], the new blocks, distinct from one
+ *                   another and from every block that the call reads;
+ *                   dst_blocks_per_seq * 16 >= min(keep, max_context_len). Entries past
+ *                   ceil(new length / 16) are not read, rows past the new length are
+ *                   left alone.
+ *   new_weights   : fp32 [B][Hk][dst_blocks_per_seq * 16], zero past the new length;
+ *                   not `weights`
+ *   new_context_lens : int32 [B], min(n, keep); not `context_lens`
+ *   kept          : int32 [B][Hk][keep], the kept entries' old indices in order, -1 past
+ *                   the new length
+ *   keep >= 1, sinks >= 0, recent >= 0, sinks + recent <= keep
+ *   k_scales, v_scales : block8 pools' scales, updated for the new blocks; NULL otherwise
+ * The old blocks and tables are only read. Two launches.
+ */
+int pa_evict(void *k_cache, void *v_cache, float *k_scales, float *v_scales, const float *weights,
+             int32_t weights_width, const int32_t *block_tables, int32_t max_blocks_per_seq,
+             const int32_t *context_lens, const int32_t *dst_block_tables, int32_t dst_blocks_per_seq,
+             float *new_weights, int32_t *new_context_lens, int32_t *kept, int32_t num_seqs, int32_t max_context_len,
+             int32_t keep, int32_t sinks, int32_t recent, const pa_shape *shape, void *stream);
 
 /*
  * pa_get_status: synchronize `stream`, copy the device status word of the

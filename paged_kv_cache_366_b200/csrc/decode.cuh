@@ -192,6 +192,9 @@ struct DecodeParams {
     int max_context_len;
     float scale_log2;  // softmax scale * log2(e) (times k_scale for an FP8 cache)
     float v_scale;     // 1, or the FP8 value scale
+    float *scores;     // weight-counting decode: [B * Hk][score_rows][G] scores in the log2 domain
+    float *lse;        // weight-counting decode: [B][H], log2 of each head's softmax denominator
+    int score_rows;    // entries of one unit in `scores`, a multiple of the block size
 };
 
 // Position in the flat (sequence, KV head, block) list.
@@ -237,9 +240,121 @@ __device__ __forceinline__ int slice_of(long long f, long long N, int W) {
     return static_cast<int>(((f + 1) * W - 1) / N);
 }
 
+// The start of a decode CTA of WARPS warps (the whole CTA takes part): the
+// list's block count N, its number of slices WS, and for each warp the first
+// block of its slice in `starts` (5 ints: b, hk, blk, c, nblk). Rows of
+// sequences of length 0 are written as zeros here. `cum` is CHUNK entries of
+// shared memory, free again on return.
+template <typename Tq, int D, int WARPS, int CHUNK>
+__device__ __forceinline__ void decode_prologue(const DecodeParams &prm, long long *cum, int *starts, long long &N,
+                                                int &WS) {
+    constexpr int THREADS = 32 * WARPS;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int B = prm.num_seqs, Hk = prm.num_kv_heads;
+    const int cap = decode_cap(prm);
+    // While the prologue scans the lengths, bring the block tables towards L2
+    // (each CTA a 1/gridDim share, 128-byte lines), so that a warp's first
+    // table read after the prologue does not wait on HBM. Up to 8 MB of table.
+    {
+        const long long lines = (static_cast<long long>(prm.num_seqs) * prm.max_blocks_per_seq * 4 + 127) / 128;
+        if (lines <= (8LL << 20) / 128) {
+            const char *tb = reinterpret_cast<const char *>(prm.block_tables);
+            for (long long i = blockIdx.x + static_cast<long long>(gridDim.x) * threadIdx.x; i < lines;
+                 i += static_cast<long long>(gridDim.x) * THREADS)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(tb + i * 128));
+        }
+    }
+
+    // ---- prologue (the whole CTA): the total block count N, the slices, and
+    // the unit holding each warp's first block, from prefix sums of Hk * blocks
+    // over the sequences, a chunk of sequences at a time in shared memory (`cum`,
+    // CHUNK entries). With more sequences than one chunk holds, a
+    // first pass sums N.
+    N = 0;
+    if (B > CHUNK) {
+        long long part = 0;
+        for (int b = threadIdx.x; b < B; b += THREADS) {
+            const int c = clamp_context(__ldg(prm.context_lens + b), cap, false);
+            part += (c + kBlockSize - 1) / kBlockSize;
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+        if (lane == 0) cum[warp] = part;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) N += cum[w];
+        N *= Hk;
+        __syncthreads();
+    }
+    const int cta0 = static_cast<int>(blockIdx.x) * WARPS;  // first slice of this CTA
+    WS = 0;  // slices: at most one per block, so that none is empty (a unit's slices are then
+             // exactly those from the slice of its first block to that of its last)
+    {
+        long long base = 0;
+        for (int c0 = 0; c0 < B; c0 += CHUNK) {
+            const int n = min(CHUNK, B - c0);
+            for (int i = threadIdx.x; i < n; i += THREADS) {
+                const int c = clamp_context(__ldg(prm.context_lens + c0 + i), cap, blockIdx.x == 0);
+                cum[i] = static_cast<long long>((c + kBlockSize - 1) / kBlockSize) * Hk;
+            }
+            __syncthreads();
+            if (warp == 0) {  // inclusive scan, 32 entries per step
+                long long carry = base;
+                for (int i0 = 0; i0 < n; i0 += 32) {
+                    long long v = i0 + lane < n ? cum[i0 + lane] : 0;
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const long long t = __shfl_up_sync(0xffffffffu, v, off);
+                        if (lane >= off) v += t;
+                    }
+                    v += carry;
+                    if (i0 + lane < n) cum[i0 + lane] = v;
+                    carry = __shfl_sync(0xffffffffu, v, 31);
+                }
+            }
+            __syncthreads();
+            if (B <= CHUNK) N = cum[n - 1];  // one chunk: the total comes with the scan
+            WS = static_cast<int>(min(static_cast<long long>(gridDim.x) * WARPS, N));
+            // a sequence of length 0 has no blocks: CTA b % gridDim.x writes its zero rows
+            for (int i = threadIdx.x; i < n; i += THREADS) {
+                const long long hi = cum[i], lo = i ? cum[i - 1] : base;
+                const int b = c0 + i;
+                if (lo >= hi && b % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x)) {
+                    Tq *o = static_cast<Tq *>(prm.out) + static_cast<size_t>(b) * prm.num_heads * D;
+                    for (int e = 0; e < prm.num_heads * D; ++e) store_out(o + e, 0.f);
+                }
+            }
+            // thread w: the first block of slice cta0 + w, if it lies in this chunk
+            const int w = threadIdx.x;
+            if (w < WARPS && cta0 + w < WS) {
+                const long long f = N * (cta0 + w) / WS;
+                if (f >= base && f < cum[n - 1]) {
+                    int lo_i = 0, hi_i = n - 1;  // the first sequence whose inclusive sum exceeds f
+                    while (lo_i < hi_i) {
+                        const int mid = (lo_i + hi_i) / 2;
+                        if (cum[mid] > f) hi_i = mid;
+                        else lo_i = mid + 1;
+                    }
+                    const long long lo = lo_i ? cum[lo_i - 1] : base;
+                    const int nblk = static_cast<int>((cum[lo_i] - lo) / Hk);
+                    const long long r = f - lo;
+                    starts[5 * w + 0] = c0 + lo_i;
+                    starts[5 * w + 1] = static_cast<int>(r / nblk);
+                    starts[5 * w + 2] = static_cast<int>(r % nblk);
+                    starts[5 * w + 3] = clamp_context(__ldg(prm.context_lens + c0 + lo_i), cap, false);
+                    starts[5 * w + 4] = nblk;
+                }
+            }
+            base = cum[n - 1];
+            __syncthreads();
+        }
+    }
+}
+
 // Tq: element type of q and out. Tc: element type of the caches (the same, or
-// FP8 E4M3 codes with bf16 q/out).
-template <typename Tq, typename Tc, int D, int G>
+// FP8 E4M3 codes with bf16 q/out). EMIT: also write every score and, for units
+// in one slice, the heads' log2 denominators (attn_weights.cuh reads them).
+template <typename Tq, typename Tc, int D, int G, bool EMIT = false>
 __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
     decode_kernel(const DecodeParams prm, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v) {
@@ -248,8 +363,7 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
     constexpr int VP = C::VE / 2;  // packed pairs per chunk
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rg = lane / C::L, j = lane % C::L;
-    const int B = prm.num_seqs, Hk = prm.num_kv_heads;
-    const int cap = decode_cap(prm);
+    const int Hk = prm.num_kv_heads;
 
     extern __shared__ __align__(128) unsigned char smem[];
     int *starts = reinterpret_cast<int *>(smem + C::OFF_MISC);  // per warp: b, hk, blk, c, nblk of its first block
@@ -282,105 +396,10 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
     // waits for this grid to finish before reading anything.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // While the prologue scans the lengths, bring the block tables towards L2
-    // (each CTA a 1/gridDim share, 128-byte lines), so that a warp's first
-    // table read after the prologue does not wait on HBM. Up to 8 MB of table.
-    {
-        const long long lines = (static_cast<long long>(prm.num_seqs) * prm.max_blocks_per_seq * 4 + 127) / 128;
-        if (lines <= (8LL << 20) / 128) {
-            const char *tb = reinterpret_cast<const char *>(prm.block_tables);
-            for (long long i = blockIdx.x + static_cast<long long>(gridDim.x) * threadIdx.x; i < lines;
-                 i += static_cast<long long>(gridDim.x) * C::THREADS)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(tb + i * 128));
-        }
-    }
-
-    // ---- prologue (the whole CTA): the total block count N, the slices, and
-    // the unit holding each warp's first block, from prefix sums of Hk * blocks
-    // over the sequences, a chunk of sequences at a time in shared memory (the
-    // ring is not in use yet). With more sequences than one chunk holds, a
-    // first pass sums N.
-    constexpr int CHUNK = C::RING_BYTES / 8;
-    long long *cum = reinterpret_cast<long long *>(smem);
-    long long N = 0;
-    if (B > CHUNK) {
-        long long part = 0;
-        for (int b = threadIdx.x; b < B; b += C::THREADS) {
-            const int c = clamp_context(__ldg(prm.context_lens + b), cap, false);
-            part += (c + kBlockSize - 1) / kBlockSize;
-        }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-        if (lane == 0) cum[warp] = part;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) N += cum[w];
-        N *= Hk;
-        __syncthreads();
-    }
+    long long N;
+    int WS;  // slices: at most one per block
+    decode_prologue<Tq, D, C::WARPS, C::RING_BYTES / 8>(prm, reinterpret_cast<long long *>(smem), starts, N, WS);
     const int cta0 = static_cast<int>(blockIdx.x) * C::WARPS;  // first slice of this CTA
-    int WS = 0;  // slices: at most one per block, so that none is empty (a unit's slices are then
-                 // exactly those from the slice of its first block to that of its last)
-    {
-        long long base = 0;
-        for (int c0 = 0; c0 < B; c0 += CHUNK) {
-            const int n = min(CHUNK, B - c0);
-            for (int i = threadIdx.x; i < n; i += C::THREADS) {
-                const int c = clamp_context(__ldg(prm.context_lens + c0 + i), cap, blockIdx.x == 0);
-                cum[i] = static_cast<long long>((c + kBlockSize - 1) / kBlockSize) * Hk;
-            }
-            __syncthreads();
-            if (warp == 0) {  // inclusive scan, 32 entries per step
-                long long carry = base;
-                for (int i0 = 0; i0 < n; i0 += 32) {
-                    long long v = i0 + lane < n ? cum[i0 + lane] : 0;
-#pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const long long t = __shfl_up_sync(0xffffffffu, v, off);
-                        if (lane >= off) v += t;
-                    }
-                    v += carry;
-                    if (i0 + lane < n) cum[i0 + lane] = v;
-                    carry = __shfl_sync(0xffffffffu, v, 31);
-                }
-            }
-            __syncthreads();
-            if (B <= CHUNK) N = cum[n - 1];  // one chunk: the total comes with the scan
-            WS = static_cast<int>(min(static_cast<long long>(gridDim.x) * C::WARPS, N));
-            // a sequence of length 0 has no blocks: CTA b % gridDim.x writes its zero rows
-            for (int i = threadIdx.x; i < n; i += C::THREADS) {
-                const long long hi = cum[i], lo = i ? cum[i - 1] : base;
-                const int b = c0 + i;
-                if (lo >= hi && b % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x)) {
-                    Tq *o = static_cast<Tq *>(prm.out) + static_cast<size_t>(b) * prm.num_heads * D;
-                    for (int e = 0; e < prm.num_heads * D; ++e) store_out(o + e, 0.f);
-                }
-            }
-            // thread w: the first block of slice cta0 + w, if it lies in this chunk
-            const int w = threadIdx.x;
-            if (w < C::WARPS && cta0 + w < WS) {
-                const long long f = N * (cta0 + w) / WS;
-                if (f >= base && f < cum[n - 1]) {
-                    int lo_i = 0, hi_i = n - 1;  // the first sequence whose inclusive sum exceeds f
-                    while (lo_i < hi_i) {
-                        const int mid = (lo_i + hi_i) / 2;
-                        if (cum[mid] > f) hi_i = mid;
-                        else lo_i = mid + 1;
-                    }
-                    const long long lo = lo_i ? cum[lo_i - 1] : base;
-                    const int nblk = static_cast<int>((cum[lo_i] - lo) / Hk);
-                    const long long r = f - lo;
-                    starts[5 * w + 0] = c0 + lo_i;
-                    starts[5 * w + 1] = static_cast<int>(r / nblk);
-                    starts[5 * w + 2] = static_cast<int>(r % nblk);
-                    starts[5 * w + 3] = clamp_context(__ldg(prm.context_lens + c0 + lo_i), cap, false);
-                    starts[5 * w + 4] = nblk;
-                }
-            }
-            base = cum[n - 1];
-            __syncthreads();
-        }
-    }
     if (cta0 >= WS) return;
     // ---- from here on every warp runs alone on its slice
     const int slice = cta0 + warp;
@@ -564,6 +583,15 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
             prm.ws_m[slot * G + lane] = m;
             prm.ws_l[slot * G + lane] = l;
         }
+        if constexpr (EMIT) {
+            if (whole && lane < G) {
+                float lse = 0.f;
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    if (lane == g) lse = m_head[g] + log2f(l_head[g]);
+                prm.lse[static_cast<size_t>(u) * G + lane] = lse;
+            }
+        }
         if (lane == 0 && u_lo >= s_lo) {  // the unit starts in this slice: where its partials are
             int *rec = prm.ws_unit + 2 * static_cast<size_t>(u);
             rec[0] = slice;
@@ -635,6 +663,16 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
             if (n_valid < kBlockSize && t_own >= n_valid) {
 #pragma unroll
                 for (int f = 0; f < C::NFIN; ++f) sc[f] = -CUDART_INF_F;
+            }
+
+            if constexpr (EMIT) {  // lanes holding copies of the same scores write them once
+                if (t_own < n_valid && (C::DUP == 1 || (j & (C::DUP - 1)) == 0)) {
+                    float *row = prm.scores +
+                                 ((static_cast<size_t>(cc.b) * Hk + cc.hk) * prm.score_rows + cc.blk * kBlockSize +
+                                  t_own) * G + hmask;
+#pragma unroll
+                    for (int f = 0; f < C::NFIN; ++f) row[f] = sc[f];
+                }
             }
 
             // ---- online softmax. The max of a head moves (and O, l are rescaled)
@@ -754,7 +792,8 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
 // slices from the lengths before the wait; larger ones read the records.
 constexpr int kMergeScanSeqs = 256;
 
-template <typename T, int G, int D, int MG>
+// EMIT: also write the log2 denominators of the cut units' heads.
+template <typename T, int G, int D, int MG, bool EMIT = false>
 __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParams prm) {
     __shared__ float4 sh_o[MG][32];
     __shared__ float sh_m[MG][32], sh_l[MG][32];
@@ -835,7 +874,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         }
         M = mc;
     }
-    float Lt = Lsum;
+    float Lt = Lsum, Mt = M;
     float4 Ot = O;
     if constexpr (MG > 1) {
         sh_o[grp][lane] = O;
@@ -843,7 +882,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         sh_l[grp][lane] = Lsum;
         __syncthreads();
         if (grp != 0) return;
-        float Mt = sh_m[0][lane];
+        Mt = sh_m[0][lane];
 #pragma unroll
         for (int w = 1; w < MG; ++w) Mt = fmaxf(Mt, sh_m[w][lane]);
         Lt = 0.f;
@@ -862,6 +901,9 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         }
     }
     if (!col) return;
+    if constexpr (EMIT) {
+        if (d == 0) prm.lse[static_cast<size_t>(u) * G + g] = Mt + log2f(Lt);
+    }
     const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
     Ot.x *= inv;
     Ot.y *= inv;

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <algorithm>
 #include <atomic>
 
 #include "pa_common.cuh"
@@ -71,7 +72,7 @@ int cache_elem_bytes(const pa_shape *s) { return s->kv_fp8 ? 1 : elem_bytes(s); 
 // the largest shared-memory carveout, set here once per device), or, without
 // a device, the compile-time estimate. The grid is sized from it, so every
 // slice's CTA is resident from the start.
-template <typename Tq, typename Tc, int D, int G>
+template <typename Tq, typename Tc, int D, int G, bool EMIT = false>
 int resident_of() {
     using C = pa::DecodeCfg<Tc, D, G>;
     static std::atomic<int> cached[kMaxDevices];
@@ -82,7 +83,7 @@ int resident_of() {
     }
     int n = cached[dev].load(std::memory_order_acquire);
     if (n > 0) return n;
-    auto kernel = pa::decode_kernel<Tq, Tc, D, G>;
+    auto kernel = pa::decode_kernel<Tq, Tc, D, G, EMIT>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
@@ -144,12 +145,11 @@ int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 // maxima and sums [slots][G] each, then int32 (first slice, slices) records
 // [B][Hk]; each part 16-byte aligned.
 int decode_geometry(int32_t num_seqs, int32_t max_context_len, int32_t requested, const pa_shape *s,
-                    DecodeGeometry *g) {
+                    DecodeGeometry *g, const DecodeFit &fit) {
     if (num_seqs < 0 || max_context_len < 0) return PA_ERR_INVALID_ARGUMENT;
     if (requested < 0 || (requested > 0 && (requested % 64 != 0))) return PA_ERR_INVALID_ARGUMENT;
     const int64_t units = static_cast<int64_t>(num_seqs) * s->num_kv_heads;
     const int64_t n_max = units * ((max_context_len + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE);
-    const DecodeFit fit = decode_fit(s);
     int64_t slices;
     if (requested > 0) {
         slices = (n_max * PA_BLOCK_SIZE + requested - 1) / requested;
@@ -170,10 +170,42 @@ int decode_geometry(int32_t num_seqs, int32_t max_context_len, int32_t requested
     return PA_OK;
 }
 
+int decode_geometry(int32_t num_seqs, int32_t max_context_len, int32_t requested, const pa_shape *s,
+                    DecodeGeometry *g) {
+    return decode_geometry(num_seqs, max_context_len, requested, s, g, decode_fit(s));
+}
+
+// The partials' places in a workspace of at least g.ws_bytes.
+void place_partials(pa::DecodeParams *prm, const DecodeGeometry &g, const pa_shape *s, void *workspace) {
+    const int gq = s->num_heads / s->num_kv_heads;
+    char *w = static_cast<char *>(workspace);
+    const int64_t o_bytes = g.slots * gq * s->head_dim * 4, ml_bytes = round16(g.slots * gq * 4);
+    prm->ws_o = reinterpret_cast<float *>(w);
+    prm->ws_m = reinterpret_cast<float *>(w + o_bytes);
+    prm->ws_l = reinterpret_cast<float *>(w + o_bytes + ml_bytes);
+    prm->ws_unit = reinterpret_cast<int *>(w + o_bytes + 2 * ml_bytes);
+}
+
 // The two launches of a decode: the partition pass and the merge.
 enum DecodeParts { kPartials = 1, kMerge = 2, kBoth = 3 };
 
-template <typename Tq, typename Tc, int D, int G>
+// The merge of cut units, with the caller's stream and launch attributes.
+template <typename Tq, int G, int D, bool EMIT>
+int launch_merge(const pa::DecodeParams &p, const DecodeGeometry &geo, int warps, cudaLaunchConfig_t cfg) {
+    // Four warps per unit when units average 16 slices or more (long
+    // contexts): their slices are merged four ways at once. One otherwise:
+    // fewer, smaller CTAs launch and finish sooner.
+    const int64_t units = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
+    const bool wide = static_cast<int64_t>(geo.ctas) * warps >= 16 * units;
+    cfg.gridDim = dim3(static_cast<unsigned>(units), (G * D + 127) / 128);
+    cfg.blockDim = dim3(wide ? 128 : 32);
+    cfg.dynamicSmemBytes = 0;
+    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 4, EMIT>, p)
+                               : cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 1, EMIT>, p);
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+template <typename Tq, typename Tc, int D, int G, bool EMIT>
 int launch_decode(const pa::DecodeParams &prm, const DecodeGeometry &geo, int parts, cudaStream_t st) {
     using C = pa::DecodeCfg<Tc, D, G>;
     // Both kernels are programmatic dependent launches: each starts launching
@@ -189,7 +221,7 @@ int launch_decode(const pa::DecodeParams &prm, const DecodeGeometry &geo, int pa
     pa::DecodeParams p = prm;
     p.warps_total = geo.ctas * C::WARPS;
     if (parts & kPartials) {
-        resident_of<Tq, Tc, D, G>();  // sets the kernel's shared-memory attributes on this device
+        resident_of<Tq, Tc, D, G, EMIT>();  // sets the kernel's shared-memory attributes on this device
         CUtensorMap tm_k{}, tm_v{};
         const uint64_t rows = static_cast<uint64_t>(prm.num_blocks) * pa::kBlockSize;
         if (!pa::encode_3d(&tm_k, prm.k_cache, D, prm.num_kv_heads, rows, sizeof(Tc), D, 1, pa::kBlockSize,
@@ -200,32 +232,20 @@ int launch_decode(const pa::DecodeParams &prm, const DecodeGeometry &geo, int pa
         cfg.gridDim = dim3(geo.ctas);
         cfg.blockDim = dim3(C::THREADS);
         cfg.dynamicSmemBytes = C::SMEM;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, pa::decode_kernel<Tq, Tc, D, G>, p, tm_k, tm_v);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, pa::decode_kernel<Tq, Tc, D, G, EMIT>, p, tm_k, tm_v);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    if (parts & kMerge) {
-        // Four warps per unit when units average 16 slices or more (long
-        // contexts): their slices are merged four ways at once. One otherwise:
-        // fewer, smaller CTAs launch and finish sooner.
-        const int64_t units = static_cast<int64_t>(prm.num_seqs) * prm.num_kv_heads;
-        const bool wide = static_cast<int64_t>(geo.ctas) * C::WARPS >= 16 * units;
-        cfg.gridDim = dim3(static_cast<unsigned>(units), (G * D + 127) / 128);
-        cfg.blockDim = dim3(wide ? 128 : 32);
-        cfg.dynamicSmemBytes = 0;
-        const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 4>, p)
-                                   : cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 1>, p);
-        if (e != cudaSuccess) return cuda_fail(e);
-    }
+    if (parts & kMerge) return launch_merge<Tq, G, D, EMIT>(p, geo, C::WARPS, cfg);
     return PA_OK;
 }
 
-template <typename Tq, typename Tc, int D>
+template <typename Tq, typename Tc, int D, bool EMIT = false>
 int dispatch_g(int g, const pa::DecodeParams &prm, const DecodeGeometry &geo, int parts, cudaStream_t st) {
     switch (g) {
-        case 1: return launch_decode<Tq, Tc, D, 1>(prm, geo, parts, st);
-        case 2: return launch_decode<Tq, Tc, D, 2>(prm, geo, parts, st);
-        case 4: return launch_decode<Tq, Tc, D, 4>(prm, geo, parts, st);
-        case 8: return launch_decode<Tq, Tc, D, 8>(prm, geo, parts, st);
+        case 1: return launch_decode<Tq, Tc, D, 1, EMIT>(prm, geo, parts, st);
+        case 2: return launch_decode<Tq, Tc, D, 2, EMIT>(prm, geo, parts, st);
+        case 4: return launch_decode<Tq, Tc, D, 4, EMIT>(prm, geo, parts, st);
+        case 8: return launch_decode<Tq, Tc, D, 8, EMIT>(prm, geo, parts, st);
         default: return PA_ERR_UNSUPPORTED;
     }
 }
@@ -319,15 +339,7 @@ int decode_call(void *out, const void *q, const void *k_cache, const void *v_cac
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!workspace || workspace_bytes < g.ws_bytes) return PA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PA_ERR_ALIGNMENT;
-    {
-        const int gq = shape->num_heads / shape->num_kv_heads;
-        char *w = static_cast<char *>(workspace);
-        const int64_t o_bytes = g.slots * gq * shape->head_dim * 4, ml_bytes = round16(g.slots * gq * 4);
-        prm.ws_o = reinterpret_cast<float *>(w);
-        prm.ws_m = reinterpret_cast<float *>(w + o_bytes);
-        prm.ws_l = reinterpret_cast<float *>(w + o_bytes + ml_bytes);
-        prm.ws_unit = reinterpret_cast<int *>(w + o_bytes + 2 * ml_bytes);
-    }
+    place_partials(&prm, g, shape, workspace);
     prm.out = out;
     prm.q = q;
     prm.k_cache = k_cache;
@@ -560,3 +572,5 @@ int pa_get_status(uint32_t *status, void *stream) {
 }
 
 }  // extern "C"
+
+#include "cache_ops_api.cuh"

@@ -42,12 +42,29 @@ class PaShape(ctypes.Structure):
     ]
 
 
+class PaRopePlan(ctypes.Structure):
+    """pa_rope_plan: what pa_rope_init makes and the rotary calls take."""
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("mscale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("step", ctypes.c_uint64 * 64),
+    ]
+
+
 EXPORTED = [
     "pa_reshape_and_cache", "pa_decode_workspace_bytes", "pa_decode", "pa_decode_partials", "pa_decode_merge",
     "pa_prefill_chunk",
     "pa_get_status", "pa_strerror", "pa_last_cuda_error", "pa_abi_version", "pa_decode_noalloc",
     "pa_copy_blocks", "pa_swap_blocks",
+    "pa_rope_init", "pa_rope", "pa_rope_and_cache", "pa_cache_block8", "pa_decode_block8_workspace_bytes",
+    "pa_decode_block8", "pa_decode_weights_workspace_bytes", "pa_decode_weights", "pa_evict",
 ]
+
+PA_KV_BLOCK_E4M3, PA_KV_BLOCK_INT8 = 2, 3
+PA_ROPE_MAX_DIM = 128
+_ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 PA_ERR_SCRATCH_LIMIT = -7
 PA_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -74,6 +91,20 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_copy_blocks.restype = ctypes.c_int
     lib.pa_swap_blocks.argtypes = [P, P, P, I64, I64, I64, I64, P]
     lib.pa_swap_blocks.restype = ctypes.c_int
+    RP, D = ctypes.POINTER(PaRopePlan), ctypes.c_double
+    lib.pa_rope_init.argtypes = [RP, I32, I32, D, I32, D, D, D, D, D]
+    lib.pa_rope.argtypes = [P, P, P, P, I64, I64, P, I64, RP, SP, P]
+    lib.pa_rope_and_cache.argtypes = [P, P, P, P, I64, I64, I64, P, P, P, P, I64, RP, SP, P]
+    lib.pa_cache_block8.argtypes = [P, P, P, P, P, P, P, I64, SP, P]
+    lib.pa_decode_block8.argtypes = [P, P, P, P, P, P, P, I32, P, I32, I32, F, I32, P, I64, SP, P]
+    lib.pa_decode_weights.argtypes = [P, P, I32, P, P, P, P, P, P, I32, P, I32, I32, F, I32, P, I64, SP, P]
+    lib.pa_evict.argtypes = [P, P, P, P, P, I32, P, I32, P, P, I32, P, P, P, I32, I32, I32, I32, I32, SP, P]
+    for name in ("pa_rope_init", "pa_rope", "pa_rope_and_cache", "pa_cache_block8", "pa_decode_block8",
+                 "pa_decode_weights", "pa_evict"):
+        getattr(lib, name).restype = ctypes.c_int
+    for name in ("pa_decode_block8_workspace_bytes", "pa_decode_weights_workspace_bytes"):
+        getattr(lib, name).argtypes = [I32, I32, I32, SP]
+        getattr(lib, name).restype = I64
     lib.pa_get_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), P]
     lib.pa_get_status.restype = ctypes.c_int
     lib.pa_strerror.argtypes = [ctypes.c_int]
@@ -297,6 +328,218 @@ def pa_swap_blocks(dst, src, block_pairs, stream=None) -> None:
     _check("pa_swap_blocks", lib.pa_swap_blocks(_any_ptr(dst), _any_ptr(src), _any_ptr(block_pairs),
                                                 block_pairs.numel() // 2, src.shape[0], dst.shape[0], bb,
                                                 _stream(stream)))
+
+
+# ---- rotary positions, the block-scaled 8-bit cache, weight-counting decode, eviction ----
+
+
+def pa_rope_init(rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, low: float = 1.0, high: float = 32.0, original_len: float = 0.0,
+                 mscale: float = 1.0) -> PaRopePlan:
+    """Plan of a rotary embedding of the first rot_dim dims. scaling: none, linear, base or parts."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError("scaling must be one of %s, got %r" % (sorted(_ROPE_SCALING), scaling))
+    plan = PaRopePlan()
+    _check("pa_rope_init", lib.pa_rope_init(ctypes.byref(plan), int(rot_dim), 1 if interleaved else 0, float(base),
+                                            _ROPE_SCALING[scaling], float(factor), float(low), float(high),
+                                            float(original_len), float(mscale)))
+    return plan
+
+
+def _rows(t: torch.Tensor, name: str, tokens: int, heads: int, dim: int):
+    """Pointer and token stride (elements) of [T, heads, D] rows whose last two dims are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    if t.shape != (tokens, heads, dim):
+        raise ValueError("%s must be [%d, %d, %d], got %s" % (name, tokens, heads, dim, tuple(t.shape)))
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
+        raise ValueError("%s must have contiguous heads (any token stride)" % name)
+    return ctypes.c_void_p(t.data_ptr()), (stride[0] if tokens > 1 else heads * dim)
+
+
+def pa_rope(q_out, k_out, q, k, positions, plan: PaRopePlan, stream=None) -> None:
+    """Rotate q [T, H, D] and k [T, Hk, D] by position (token strides are free; in place where contiguous)."""
+    _same_dtype(q_out, k_out, q, k)
+    _int(positions, torch.int64, "positions")
+    T, H, D = q.shape
+    Hk = k.shape[1]
+    if q_out.shape != q.shape or k_out.shape != k.shape or positions.shape != (T,):
+        raise ValueError("q, q_out [T, H, D]; k, k_out [T, Hk, D]; positions [T]")
+    qp, qs = _rows(q, "q", T, H, D)
+    kp, ks = _rows(k, "k", T, Hk, D)
+    shape = PaShape(num_heads=H, num_kv_heads=Hk, head_dim=D, block_size=BLOCK_SIZE, num_blocks=1,
+                    dtype=_dtype_code(q.dtype))
+    _check("pa_rope", lib.pa_rope(_ptr(q_out), _ptr(k_out), qp, kp, qs, ks, _ptr(positions), T, ctypes.byref(plan),
+                                  ctypes.byref(shape), _stream(stream)))
+
+
+def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, plan: PaRopePlan, stream=None,
+                      k_scale: float = 0.0, v_scale: float = 0.0) -> None:
+    """Rotate q [T, H, D] into q_out, and write the rotated k and v [T, Hk, D] to their slots of the pool."""
+    _same_dtype_kv((q_out, q, k, v), (k_cache, v_cache))
+    _int(slot_mapping, torch.int64, "slot_mapping")
+    _int(positions, torch.int64, "positions")
+    T, H, D = q.shape
+    shape = shape_of(k_cache, H, k_scale, v_scale)
+    Hk = shape.num_kv_heads
+    if (q_out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[3] != D
+            or positions.shape != (T,) or slot_mapping.shape != (T,)):
+        raise ValueError("q, q_out [T, H, D]; caches [NB, 16, Hk, D]; slot_mapping, positions [T]")
+    qp, qs = _rows(q, "q", T, H, D)
+    kp, ks = _rows(k, "k", T, Hk, D)
+    vp, vs = _rows(v, "v", T, Hk, D)
+    _check("pa_rope_and_cache",
+           lib.pa_rope_and_cache(_ptr(q_out), qp, kp, vp, qs, ks, vs, _ptr(k_cache), _ptr(v_cache),
+                                 _ptr(slot_mapping), _ptr(positions), T, ctypes.byref(plan), ctypes.byref(shape),
+                                 _stream(stream)))
+
+
+def shape_of_block8(k_codes: torch.Tensor, num_heads: int) -> PaShape:
+    """pa_shape of a block8 pool [NB, 16, Hk, D]: uint8 E4M3 codes or int8 codes, beside bf16 q and out."""
+    if k_codes.dim() != 4:
+        raise ValueError("codes must be [num_blocks, block_size, num_kv_heads, head_dim]")
+    if k_codes.dtype not in (torch.uint8, torch.int8):
+        raise ValueError("block8 codes are uint8 (E4M3) or int8, got %s" % k_codes.dtype)
+    nb, bs, hk, d = k_codes.shape
+    return PaShape(num_heads=int(num_heads), num_kv_heads=hk, head_dim=d, block_size=bs, num_blocks=nb,
+                   dtype=PA_DTYPE_BF16,
+                   kv_fp8=PA_KV_BLOCK_E4M3 if k_codes.dtype == torch.uint8 else PA_KV_BLOCK_INT8)
+
+
+def _check_block8(k_codes, v_codes, k_scales, v_scales):
+    if v_codes.shape != k_codes.shape or v_codes.dtype != k_codes.dtype:
+        raise ValueError("k_codes and v_codes must have one shape and dtype")
+    want = (k_codes.shape[0], k_codes.shape[2])
+    for t in (k_scales, v_scales):
+        if t.dtype != torch.float32 or t.shape != want:
+            raise ValueError("scales must be float32 [num_blocks, num_kv_heads]")
+
+
+def _pool_shape(k_cache, v_cache, num_heads, k_scale, v_scale, k_scales, v_scales) -> PaShape:
+    """The shape of a plain pool, or of a block8 pool where its scales are given."""
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("give both k_scales and v_scales, or neither")
+    if k_scales is not None:
+        _check_block8(k_cache, v_cache, k_scales, v_scales)
+        return shape_of_block8(k_cache, num_heads)
+    _same_dtype(k_cache, v_cache)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    return shape_of(k_cache, num_heads, k_scale, v_scale)
+
+
+def pa_cache_block8(k, v, k_codes, v_codes, k_scales, v_scales, slot_mapping, stream=None) -> None:
+    """Append new tokens' bf16 K/V rows to a block8 pool; the tokens of one block are neighbours in the call."""
+    shape = shape_of_block8(k_codes, k_codes.shape[2])
+    _check_block8(k_codes, v_codes, k_scales, v_scales)
+    _int(k, torch.bfloat16, "k")
+    _int(v, torch.bfloat16, "v")
+    _int(slot_mapping, torch.int64, "slot_mapping")
+    if k.shape[1:] != k_codes.shape[2:] or v.shape != k.shape or slot_mapping.shape != (k.shape[0],):
+        raise ValueError("k, v must be [T, Hk, D] matching the pool; slot_mapping [T]")
+    _check("pa_cache_block8",
+           lib.pa_cache_block8(_ptr(k), _ptr(v), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales),
+                               _ptr(slot_mapping), k.shape[0], ctypes.byref(shape), _stream(stream)))
+
+
+def pa_decode_block8_workspace_bytes(num_seqs: int, max_context_len: int, partition_tokens: int,
+                                     shape: PaShape) -> int:
+    n = lib.pa_decode_block8_workspace_bytes(int(num_seqs), int(max_context_len), int(partition_tokens),
+                                             ctypes.byref(shape))
+    if n < 0:
+        raise PaError("pa_decode_block8_workspace_bytes", int(n))
+    return int(n)
+
+
+def _check_decode(out, q, k_cache, block_tables, context_lens):
+    _int(block_tables, torch.int32, "block_tables")
+    _int(context_lens, torch.int32, "context_lens")
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
+        raise ValueError("q must be [B, H, D] with the pool's D")
+    B = q.shape[0]
+    if out.shape != q.shape or block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("q, out [B, H, D]; block_tables [B, MB]; context_lens [B]")
+
+
+def pa_decode_block8(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens, max_context_len: int,
+                     scale: float, partition_tokens: int = 0, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """pa_decode over a block8 pool: uint8 (E4M3) or int8 codes with fp32 scales [NB, Hk]."""
+    _check_block8(k_codes, v_codes, k_scales, v_scales)
+    _int(q, torch.bfloat16, "q")
+    _int(out, torch.bfloat16, "out")
+    _check_decode(out, q, k_codes, block_tables, context_lens)
+    shape = shape_of_block8(k_codes, q.shape[1])
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("pa_decode_block8",
+           lib.pa_decode_block8(_ptr(out), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales),
+                                _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), q.shape[0],
+                                int(max_context_len), float(scale), int(partition_tokens), _ptr(workspace), ws_bytes,
+                                ctypes.byref(shape), _stream(stream)))
+
+
+def pa_decode_weights_workspace_bytes(num_seqs: int, max_context_len: int, partition_tokens: int,
+                                      shape: PaShape) -> int:
+    n = lib.pa_decode_weights_workspace_bytes(int(num_seqs), int(max_context_len), int(partition_tokens),
+                                              ctypes.byref(shape))
+    if n < 0:
+        raise PaError("pa_decode_weights_workspace_bytes", int(n))
+    return int(n)
+
+
+def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens, max_context_len: int,
+                      scale: float, partition_tokens: int = 0, workspace: Optional[torch.Tensor] = None, stream=None,
+                      k_scale: float = 0.0, v_scale: float = 0.0, k_scales: Optional[torch.Tensor] = None,
+                      v_scales: Optional[torch.Tensor] = None) -> None:
+    """Decode that also adds each entry's attention weight to weights [B, Hk, W] (float32, W >= max_context_len).
+
+    A pool with k_scales and v_scales [NB, Hk] is a block8 pool; a uint8 pool without them takes k_scale, v_scale.
+    """
+    _same_dtype(out, q)
+    _check_decode(out, q, k_cache, block_tables, context_lens)
+    _int(weights, torch.float32, "weights")
+    shape = _pool_shape(k_cache, v_cache, q.shape[1], k_scale, v_scale, k_scales, v_scales)
+    if _dtype_code(q.dtype) != shape.dtype:
+        raise ValueError("q and out must have the pool's dtype (bf16 beside 8-bit pools)")
+    if weights.dim() != 3 or weights.shape[:2] != (q.shape[0], shape.num_kv_heads):
+        raise ValueError("weights must be [B, Hk, W]")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("pa_decode_weights",
+           lib.pa_decode_weights(_ptr(out), _ptr(weights), weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                 _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), block_tables.shape[1],
+                                 _ptr(context_lens), q.shape[0], int(max_context_len), float(scale),
+                                 int(partition_tokens), _ptr(workspace), ws_bytes, ctypes.byref(shape),
+                                 _stream(stream)))
+
+
+def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, dst_block_tables, new_weights, new_context_lens,
+             kept, sinks: int, recent: int, max_context_len: int, stream=None,
+             k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None) -> None:
+    """Cut every sequence's cache to kept.shape[2] entries for each KV head, copied into dst_block_tables' blocks.
+
+    kept int32 [B, Hk, keep], new_weights float32 [B, Hk, 16 * dst_block_tables.shape[1]] and new_context_lens
+    int32 [B] are written; the old blocks, tables, lengths and weights are only read.
+    """
+    shape = _pool_shape(k_cache, v_cache, k_cache.shape[2], 1.0, 1.0, k_scales, v_scales)
+    for t, name in ((block_tables, "block_tables"), (context_lens, "context_lens"),
+                    (dst_block_tables, "dst_block_tables"), (new_context_lens, "new_context_lens"), (kept, "kept")):
+        _int(t, torch.int32, name)
+    _int(weights, torch.float32, "weights")
+    _int(new_weights, torch.float32, "new_weights")
+    B, Hk = context_lens.shape[0], shape.num_kv_heads
+    if (context_lens.shape != (B,) or new_context_lens.shape != (B,) or block_tables.dim() != 2
+            or dst_block_tables.dim() != 2 or block_tables.shape[0] != B or dst_block_tables.shape[0] != B
+            or kept.dim() != 3 or kept.shape[:2] != (B, Hk) or weights.dim() != 3 or weights.shape[:2] != (B, Hk)
+            or new_weights.shape != (B, Hk, dst_block_tables.shape[1] * BLOCK_SIZE)):
+        raise ValueError("context_lens, new_context_lens [B]; block_tables, dst_block_tables [B, .]; weights, kept "
+                         "[B, Hk, .]; new_weights [B, Hk, 16 * dst blocks]")
+    _check("pa_evict",
+           lib.pa_evict(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), _ptr(weights),
+                        weights.shape[2], _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+                        _ptr(dst_block_tables), dst_block_tables.shape[1], _ptr(new_weights), _ptr(new_context_lens),
+                        _ptr(kept), B, int(max_context_len), kept.shape[2], int(sinks), int(recent),
+                        ctypes.byref(shape), _stream(stream)))
 
 
 def pa_get_status(stream=None) -> int:
