@@ -194,10 +194,44 @@ int fill_decode(pa::DecodeParams *prm, DecodeGeometry *g, void *out, const void 
 
 // ---- eviction --------------------------------------------------------------------
 
+int launch_evict_select(const pa::EvictParams &p, int64_t units, cudaStream_t st) {
+    auto kernel = pa::evict_select_kernel;
+    static std::atomic<bool> ready[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kMaxDevices) return PA_ERR_DEVICE;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pa::kSelectKeys * 4);
+        if (e != cudaSuccess) return cuda_fail(e);
+        ready[dev].store(true, std::memory_order_release);
+    }
+    // CTAs of a row: as many as bring their share to kSelectShare keys, up to a portable cluster
+    int ranks = 1;
+    while (ranks < pa::kSelectMaxCluster && static_cast<int64_t>(ranks) * pa::kSelectShare < p.max_context_len)
+        ranks *= 2;
+    if (units * ranks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    const int held = std::min((p.max_context_len + ranks - 1) / ranks, pa::kSelectKeys);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(units * ranks));
+    cfg.blockDim = dim3(pa::kSelectThreads);
+    cfg.dynamicSmemBytes = held * 4;
+    e = cudaLaunchKernelEx(&cfg, kernel, p, held);
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 template <int ROW, int FMT>
 int launch_evict_copy(const pa::EvictParams &p, cudaStream_t st) {
-    const int64_t warps = static_cast<int64_t>(p.num_seqs) * p.dst_blocks * p.num_kv_heads;
-    if ((warps + 3) / 4 > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    const int64_t blocks = static_cast<int64_t>(p.num_seqs) * p.dst_blocks;
+    const int parts = FMT >= 0 ? 2 * p.num_kv_heads : p.num_kv_heads;
+    if (blocks > 0x7fffffff || (parts + 3) / 4 > 65535) return PA_ERR_UNSUPPORTED;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -205,7 +239,7 @@ int launch_evict_copy(const pa::EvictParams &p, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), (parts + 3) / 4);
     cfg.blockDim = dim3(128);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, pa::evict_copy_kernel<ROW, FMT>, p);
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
@@ -512,20 +546,7 @@ int pa_evict(void *k_cache, void *v_cache, float *k_scales, float *v_scales, con
     p.recent = recent;
     p.max_context_len = max_context_len;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    static std::atomic<bool> ready[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (dev < 0 || dev >= kMaxDevices) return PA_ERR_DEVICE;
-    if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(pa::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 pa::kSelectKeys * 4);
-        if (e != cudaSuccess) return cuda_fail(e);
-        ready[dev].store(true, std::memory_order_release);
-    }
-    const int held = std::min(max_context_len, pa::kSelectKeys);
-    pa::evict_select_kernel<<<static_cast<unsigned>(units), pa::kSelectThreads, held * 4, st>>>(p, held);
-    rc = check_launch();
+    rc = launch_evict_select(p, units, st);
     if (rc != PA_OK) return rc;
     const int row = shape->head_dim * cache_bytes(shape);
     if (is_block8(shape)) {

@@ -10,6 +10,9 @@
 // run at once.
 #pragma once
 
+#include <cooperative_groups.h>
+#include <math_constants.h>
+
 #include "block8.cuh"
 
 namespace pa {
@@ -41,235 +44,357 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 // ---- which entries stay ---------------------------------------------------------
 //
-// One CTA per (sequence, KV head): a radix select over the 32-bit keys, 11 + 11 + 10
-// bits, finds the smallest kept key and how many of its equals stay; then warps count
-// what they keep of their part of the row, a scan gives each its place, and a second
-// look writes. Bound by latency (a row of 32 K weights is 128 KB); the row's keys stay in
-// shared memory when they fit, so HBM sees them once.
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectWarps = kSelectThreads / 32;
+// A radix select over the 32-bit keys, 11 + 11 + 10 bits, finds the smallest kept key
+// and how many of its equals stay (it ends early once all keys that share the digits so
+// far stay); then warps count what they keep of their part of the row, a scan gives each
+// its place, and a second look writes. A (sequence, KV head) is the work of one CTA, or
+// of a cluster of up to 8 for long rows: each takes a contiguous share, adds the bins it
+// has keys in to the first CTA's through distributed shared memory, and that one tells
+// the others the digit. (Every CTA reading all the others' 2048 bins instead made the
+// select of 64 rows of up to 32 K weights 109 us; one CTA a row took 42.) Bound by
+// latency: up to three rounds of histogram, barrier and scan over a few thousand keys a
+// CTA, which stay in shared memory, so that HBM sees the weights once.
+constexpr int kSelectThreads = 512;
 constexpr int kSelectBins = 2048;
-constexpr int kSelectKeys = 50 * 1024;  // keys held in shared memory
+constexpr int kSelectShare = 4096;          // keys of a CTA, while 8 CTAs are enough for that
+constexpr int kSelectKeys = 50 * 1024;      // keys a CTA's shared memory holds at most
+constexpr int kSelectMaxCluster = 8;        // the portable cluster size
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams prm, int keys_held) {
+// Sum of v over the CTA's threads before this one; total over the CTA in `all`.
+template <int WARPS>
+__device__ __forceinline__ int scan_before(int v, int *warp_sums, int &all) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    int inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += t;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    const int w = lane < WARPS ? warp_sums[lane] : 0;
+    all = __reduce_add_sync(0xffffffffu, w);
+    return inc - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+}
+
+// Four CTAs an SM: a CTA mostly waits (for loads, shared-memory atomics, barriers), and
+// the rows of a batch of 64 sequences with 8 KV heads then fit the GPU at once.
+__global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const EvictParams prm, int keys_held) {
     extern __shared__ __align__(16) uint32_t select_keys[];
-    __shared__ int hist[kSelectBins];
-    __shared__ int warp_a[kSelectWarps], warp_b[kSelectWarps];
-    __shared__ int found[2];  // the digit, and the keys above it
+    constexpr int THREADS = kSelectThreads, WARPS = THREADS / 32;
+    __shared__ int hist[kSelectBins];     // this CTA's keys
+    __shared__ int total[kSelectBins];    // rank 0 of a cluster: all CTAs' keys
+    __shared__ int warp_sums[WARPS];
+    __shared__ int found[3];              // the digit, the keys above it, the keys in it
+    __shared__ int counts[2];             // this CTA's keys above the threshold, and equal to it
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int u = blockIdx.x, b = u / prm.num_kv_heads;
+    const int u = blockIdx.x / ranks, b = u / prm.num_kv_heads;
     const int tix = threadIdx.x, warp = tix / 32, lane = tix % 32;
-    const int n = clamp_context(__ldg(prm.context_lens + b), evict_cap(prm), u % prm.num_kv_heads == 0 && tix == 0);
+    const bool first = u % prm.num_kv_heads == 0 && rank == 0 && tix == 0;
+    const int n = clamp_context(__ldg(prm.context_lens + b), evict_cap(prm), first);
     const float *w = prm.weights + static_cast<size_t>(u) * prm.width;
     int *kept = prm.kept + static_cast<size_t>(u) * prm.keep;
     const int new_width = prm.dst_blocks * kBlockSize;
     float *new_w = prm.new_weights + static_cast<size_t>(u) * new_width;
     const int m = min(n, prm.keep);
-    if (u % prm.num_kv_heads == 0 && tix == 0) prm.new_lens[b] = m;
-    for (int i = m + tix; i < prm.keep; i += kSelectThreads) kept[i] = -1;
-    for (int i = m + tix; i < new_width; i += kSelectThreads) new_w[i] = 0.f;
-    if (n <= prm.keep) {
-        for (int i = tix; i < n; i += kSelectThreads) {
+    const int tid = rank * THREADS + tix, threads = ranks * THREADS;
+    if (first) prm.new_lens[b] = m;
+    for (int i = m + tid; i < prm.keep; i += threads) kept[i] = -1;
+    for (int i = m + tid; i < new_width; i += threads) new_w[i] = 0.f;
+    if (n <= prm.keep) {  // the same for the whole cluster
+        for (int i = tid; i < n; i += threads) {
             kept[i] = i;
             new_w[i] = __ldg(w + i);
         }
         return;
     }
     const int old = n - prm.recent;  // entries from here on always stay
-    const bool held = n <= keys_held;
-    auto key_of = [&](int i) -> uint32_t {
-        return i < prm.sinks || i >= old ? 0xffffffffu : weight_key(__ldg(w + i));
+    const int share = (n + ranks - 1) / ranks;
+    const int lo = min(n, rank * share), hi = min(n, lo + share);
+    const bool held = hi - lo <= keys_held;
+    auto key_from = [&](int i, float x) -> uint32_t {
+        return i < prm.sinks || i >= old ? 0xffffffffu : weight_key(x);
     };
-    if (held)
-        for (int i = tix; i < n; i += kSelectThreads) select_keys[i] = key_of(i);
+    auto key_of = [&](int i) -> uint32_t { return key_from(i, __ldg(w + i)); };
 
+    // a cluster: rank 0's totals start at zero before any peer adds to them
+    int *sums = ranks > 1 ? cluster.map_shared_rank(total, 0) : total;
+    if (ranks > 1) {
+        if (rank == 0)
+            for (int i = tix; i < kSelectBins; i += THREADS) total[i] = 0;
+        cluster.sync();
+    }
     uint32_t prefix = 0, mask = 0;  // the smallest kept key's digits so far
     int need = prm.keep;            // keys to keep among those that share them
-#pragma unroll
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const int bins = pass == 2 ? 1024 : 2048;
-        for (int i = tix; i < bins; i += kSelectThreads) hist[i] = 0;
+        for (int i = tix; i < bins; i += THREADS) hist[i] = 0;
         __syncthreads();
-        for (int i = tix; i < n; i += kSelectThreads) {
-            const uint32_t key = held ? select_keys[i] : key_of(i);
-            if ((key & mask) == prefix) atomicAdd(&hist[key >> shift & (bins - 1)], 1);
-        }
-        __syncthreads();
-        // thread t: the bins / 1024 bins from the top; the digit is where the running
-        // count from the top first reaches `need`
-        const int per = bins / kSelectThreads;
-        int c[2] = {0, 0}, sum = 0;
-        for (int i = 0; i < per; ++i) {
-            c[i] = hist[bins - 1 - (tix * per + i)];
-            sum += c[i];
-        }
-        int inc = sum;
+        if (pass == 0) {
+            for (int i0 = lo + tix; i0 < hi; i0 += 4 * THREADS) {
+                float x[4];  // loads in flight together
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += t;
-        }
-        if (lane == 31) warp_a[warp] = inc;
-        __syncthreads();
-        if (warp == 0) {
-            int t = warp_a[lane];
+                for (int j = 0; j < 4; ++j) x[j] = i0 + j * THREADS < hi ? __ldg(w + i0 + j * THREADS) : 0.f;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int p = __shfl_up_sync(0xffffffffu, t, off);
-                if (lane >= off) t += p;
+                for (int j = 0; j < 4; ++j) {
+                    const int i = i0 + j * THREADS;
+                    if (i < hi) {
+                        const uint32_t key = key_from(i, x[j]);
+                        if (held) select_keys[i - lo] = key;
+                        atomicAdd(&hist[key >> shift], 1);
+                    }
+                }
             }
-            warp_b[lane] = t;
+        } else {
+#pragma unroll 4
+            for (int i = lo + tix; i < hi; i += THREADS) {
+                const uint32_t key = held ? select_keys[i - lo] : key_of(i);
+                if ((key & mask) == prefix) atomicAdd(&hist[key >> shift & (bins - 1)], 1);
+            }
         }
         __syncthreads();
-        int above = inc - sum + (warp ? warp_b[warp - 1] : 0);
-        for (int i = 0; i < per; ++i) {
-            if (above < need && above + c[i] >= need) {
-                found[0] = bins - 1 - (tix * per + i);
-                found[1] = above;
-            }
-            above += c[i];
+        const int *h = hist;
+        if (ranks > 1) {
+            for (int i = tix; i < bins; i += THREADS)
+                if (hist[i]) atomicAdd(&sums[i], hist[i]);
+            cluster.sync();
+            h = total;
         }
-        __syncthreads();
+        if (rank == 0) {
+            // each thread: bins / THREADS bins from the top; the digit is where the running
+            // count from the top first reaches `need`
+            constexpr int PER = kSelectBins / THREADS;
+            const int per = bins / THREADS;
+            int c[PER], sum = 0, all;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                c[i] = i < per ? h[bins - 1 - (tix * per + i)] : 0;
+                sum += c[i];
+            }
+            int above = scan_before<WARPS>(sum, warp_sums, all);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (above < need && above + c[i] >= need) {  // one thread: its digit to every CTA
+                    for (int r = 0; r < ranks; ++r) {
+                        int *f = ranks > 1 ? cluster.map_shared_rank(found, r) : found;
+                        f[0] = bins - 1 - (tix * per + i);
+                        f[1] = above;
+                        f[2] = c[i];
+                    }
+                }
+                above += c[i];
+            }
+            if (ranks > 1 && pass < 2)
+                for (int i = 0; i < per; ++i) total[bins - 1 - (tix * per + i)] = 0;
+        }
+        if (ranks > 1) cluster.sync();
+        else __syncthreads();
         prefix |= static_cast<uint32_t>(found[0]) << shift;
         mask |= static_cast<uint32_t>(bins - 1) << shift;
         need -= found[1];
-        __syncthreads();
+        if (found[2] == need) break;  // all of them stay
     }
 
-    // keys above `prefix` stay, and the first `need` equal to it
-    const int span = (n + kSelectThreads - 1) / kSelectThreads * 32;  // entries of a warp, a multiple of 32
-    const int lo = warp * span, hi = min(n, lo + span);
+    // keys whose digits are above `prefix` stay, and the first `need` of those that share it
+    const int span = (hi - lo + THREADS - 1) / THREADS * 32;  // entries of a warp, a multiple of 32
+    const int wlo = min(hi, lo + warp * span), whi = min(hi, wlo + span);
     int gt = 0, eq = 0;
-    for (int i = lo + lane; i < hi; i += 32) {
-        const uint32_t key = held ? select_keys[i] : key_of(i);
+#pragma unroll 4
+    for (int i = wlo + lane; i < whi; i += 32) {
+        const uint32_t key = (held ? select_keys[i - lo] : key_of(i)) & mask;
         gt += key > prefix;
         eq += key == prefix;
     }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-        warp_a[warp] = gt;
-        warp_b[warp] = eq;
+    int gt_all, eq_all;
+    gt = __shfl_sync(0xffffffffu, scan_before<WARPS>(gt, warp_sums, gt_all), 0);  // of the warps before
+    eq = __shfl_sync(0xffffffffu, scan_before<WARPS>(eq, warp_sums, eq_all), 0);
+    if (ranks > 1) {  // and of the CTAs before
+        if (tix == 0) {
+            counts[0] = gt_all;
+            counts[1] = eq_all;
+        }
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            const int *peer = cluster.map_shared_rank(counts, r);
+            gt += peer[0];
+            eq += peer[1];
+        }
     }
-    __syncthreads();
-    gt = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0);
-    eq = __reduce_add_sync(0xffffffffu, lane < warp ? warp_b[lane] : 0);
     const uint32_t below = (1u << lane) - 1;
-    for (int i0 = lo; i0 < hi; i0 += 32) {
+#pragma unroll 4
+    for (int i0 = wlo; i0 < whi; i0 += 32) {
         const int i = i0 + lane;
-        const uint32_t key = i < hi ? (held ? select_keys[i] : key_of(i)) : 0u;
-        const bool is_gt = i < hi && key > prefix, is_eq = i < hi && key == prefix;
+        const float x = i < whi ? __ldg(w + i) : 0.f;  // every entry's, so that loads run ahead of the counting
+        const uint32_t key = i < whi ? (held ? select_keys[i - lo] : key_from(i, x)) & mask : 0u;
+        const bool is_gt = i < whi && key > prefix, is_eq = i < whi && key == prefix;
         const uint32_t vg = __ballot_sync(0xffffffffu, is_gt), ve = __ballot_sync(0xffffffffu, is_eq);
         const int g = gt + __popc(vg & below), e = eq + __popc(ve & below);
         if (is_gt || (is_eq && e < need)) {
             const int at = g + min(e, need);
             kept[at] = i;
-            new_w[at] = __ldg(w + i);
+            new_w[at] = x;
         }
         gt += __popc(vg);
         eq += __popc(ve);
     }
+    if (ranks > 1) cluster.sync();  // no CTA leaves while a peer may read its shared memory
 }
 
 // ---- the copy --------------------------------------------------------------------
 //
-// One warp per (sequence, new block, KV head): 16 rows of K and V, each a contiguous
-// D * E bytes of a source block, to 16 rows of the new one. Bound by HBM: 2 * rows *
-// 2 * D * E bytes. A lane holds its 16-byte pieces of all 16 rows of K (then of V)
-// in registers, so that they are in flight together.
+// One warp per (sequence, new block, KV head), and for block8 pools K or V: 16 rows, each
+// a contiguous D * E bytes of a source block, to 16 rows of the new one. Bound by HBM:
+// 2 * rows * 2 * D * E bytes. A lane holds its 16-byte pieces of all 16 rows in registers,
+// so that they are in flight together. (A persistent grid whose warps look up their next
+// piece while they copy took longer, 48 against 39 us for the batch: the registers of the
+// look-ahead cost more warps than it hides.)
 //
 // FMT >= 0 (block8): a new block's rows come from blocks of different scales; the new
 // scale is the least power of two for its rows' largest magnitude, and the codes are
-// divided by the ratio, as in the write.
+// divided by the ratio, as in the write. Codes widen exactly to f16, where their largest
+// is found, and where a product with a power of two from 2^-24 to 2^15 rounds once, to
+// the new code (below 2^-24 every code becomes 0, as there). Other ratios, which only
+// scales that are not powers of two or far apart have, go through fp32.
+
+// 16 codes of one row times ratio (exact in f16) to codes.
+template <int FMT>
+__device__ __forceinline__ uint4 rescale16(const uint32_t (&h)[8], float ratio) {
+    const __half2 r2 = __float2half2_rn(ratio);
+    const uint32_t r = *reinterpret_cast<const uint32_t *>(&r2);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (FMT == kBlockE4M3) {
+            asm("{\n\t.reg .b32 a, b;\n\t.reg .b16 x, y;\n\t"
+                "mul.rn.f16x2 a, %1, %3;\n\t"
+                "mul.rn.f16x2 b, %2, %3;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f16x2 x, a;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f16x2 y, b;\n\t"
+                "mov.b32 %0, {x, y};\n\t}"
+                : "=r"(w[i])
+                : "r"(h[2 * i]), "r"(h[2 * i + 1]), "r"(r));
+        } else {
+            // code * ratio + 1536 in one rounding: an f16 whose unit is 1, its low byte the code
+            uint32_t a, b;
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(a) : "r"(h[2 * i]), "r"(r), "r"(0x66006600u));
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(b) : "r"(h[2 * i + 1]), "r"(r), "r"(0x66006600u));
+            w[i] = __byte_perm(a, b, 0x6420);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int FMT>
+__device__ __forceinline__ void widen16(const uint4 &v, uint32_t (&h)[8]) {
+    widen4_f16<FMT>(v.x, h[0], h[1]);
+    widen4_f16<FMT>(v.y, h[2], h[3]);
+    widen4_f16<FMT>(v.z, h[4], h[5]);
+    widen4_f16<FMT>(v.w, h[6], h[7]);
+}
+
+// The largest |code| of 16, NaN aside.
+__device__ __forceinline__ float largest16(const uint32_t (&h)[8]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("max.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(top) : "r"(h[i]));
+    top &= 0x7fff7fffu;
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&top));
+    return fmaxf(f.x, f.y);
+}
+
+__device__ __forceinline__ bool power_of_two(float x) { return (__float_as_uint(x) & 0x807fffffu) == 0; }
+
 template <int ROW, int FMT>
 __device__ __forceinline__ void copy_rows(unsigned char *pool, float *scales, int kept, int rows, int src_blk,
                                           long long dst_blk, int Hk, int hk) {
-    constexpr int L = ROW / 16 < 32 ? ROW / 16 : 32;  // lanes of a row
-    constexpr int RS = 32 / L;                         // rows a step
+    constexpr int L = ROW / 16;             // lanes of a row
+    constexpr int RS = 32 / L;              // rows a step
     constexpr int STEPS = kBlockSize / RS;
-    constexpr int VPL = ROW / 16 / L;                  // 16-byte pieces of a row per lane
+    static_assert(L <= 32, "a row is one 16-byte piece of up to 32 lanes");
     const int lane = threadIdx.x % 32, j = lane % L, rg = lane / L;
     const size_t pitch = static_cast<size_t>(Hk) * ROW;
-    uint4 v[STEPS][VPL];
+    uint4 v[STEPS];
     float s[STEPS];  // block8: the row's scale
+    float mine = 0.f;  // lane t: row t's
+    if constexpr (FMT >= 0) {
+        if (lane < rows && src_blk >= 0) mine = __ldcg(scales + static_cast<size_t>(src_blk) * Hk + hk);
+    }
 #pragma unroll
     for (int st = 0; st < STEPS; ++st) {
         const int t = st * RS + rg;
         const int e = __shfl_sync(0xffffffffu, kept, t), sb = __shfl_sync(0xffffffffu, src_blk, t);
-        if (t < rows && sb >= 0) {
-            const unsigned char *p =
-                pool + (static_cast<size_t>(sb) * kBlockSize + e % kBlockSize) * pitch + hk * ROW + j * 16;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) v[st][i] = __ldcs(reinterpret_cast<const uint4 *>(p + i * L * 16));
-            if constexpr (FMT >= 0) s[st] = __ldcg(scales + static_cast<size_t>(sb) * Hk + hk);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) v[st][i] = make_uint4(0u, 0u, 0u, 0u);
-            s[st] = 0.f;
-        }
+        v[st] = make_uint4(0u, 0u, 0u, 0u);
+        if (t < rows && sb >= 0)
+            v[st] = __ldcs(reinterpret_cast<const uint4 *>(
+                pool + (static_cast<size_t>(sb) * kBlockSize + e % kBlockSize) * pitch + hk * ROW + j * 16));
     }
-    float scale = 1.f;
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) s[st] = FMT >= 0 ? __shfl_sync(0xffffffffu, mine, st * RS + rg) : 0.f;
     if constexpr (FMT >= 0) {
         float amax = 0.f;
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
-            const uint32_t w[4] = {v[st][0].x, v[st][0].y, v[st][0].z, v[st][0].w};
+            uint32_t h[8];
+            widen16<FMT>(v[st], h);
+            amax = fmaxf(amax, finite_abs(largest16(h) * s[st]));
+        }
+        const int e = scale_exponent<FMT>(warp_max(amax));
+        const float scale = exp2_int(e), inv = exp2_int(-e);
+        if (lane == 0) scales[dst_blk * Hk + hk] = scale;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float f[4];
-                widen4_f32<FMT < 0 ? 0 : FMT>(w[i], f);
+        for (int st = 0; st < STEPS; ++st) {
+            const float ratio = s[st] * inv;
+            if (ratio == 1.f) continue;
+            uint32_t h[8];
+            widen16<FMT>(v[st], h);
+            if (power_of_two(ratio) && ratio <= 0x1p15f && s[st] <= 0x1p120f) {
+                v[st] = rescale16<FMT>(h, fmaxf(ratio, 0x1p-24f));
+            } else {
+                uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) amax = fmaxf(amax, finite_abs(f[e] * s[st]));
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i]));
+                    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i + 1]));
+                    w[i] = encode4<FMT>(a.x * s[st] * inv, a.y * s[st] * inv, b.x * s[st] * inv, b.y * s[st] * inv);
+                }
+                v[st] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        scale = exp2_int(scale_exponent<FMT < 0 ? 0 : FMT>(warp_max(amax)));
-        if (lane == 0) scales[dst_blk * Hk + hk] = scale;
     }
     unsigned char *dst = pool + static_cast<size_t>(dst_blk) * kBlockSize * pitch + hk * ROW + j * 16;
 #pragma unroll
     for (int st = 0; st < STEPS; ++st) {
         const int t = st * RS + rg;
         const int sb = __shfl_sync(0xffffffffu, src_blk, t);
-        if (t >= rows || sb < 0) continue;
-        if constexpr (FMT >= 0) {
-            if (s[st] != scale) {
-                const float inv = 1.f / scale;
-                uint32_t w[4] = {v[st][0].x, v[st][0].y, v[st][0].z, v[st][0].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float f[4];
-                    widen4_f32<FMT < 0 ? 0 : FMT>(w[i], f);
-                    w[i] = encode4<FMT < 0 ? 0 : FMT>(f[0] * s[st] * inv, f[1] * s[st] * inv, f[2] * s[st] * inv,
-                                                      f[3] * s[st] * inv);
-                }
-                v[st][0] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) __stcs(reinterpret_cast<uint4 *>(dst + t * pitch + i * L * 16), v[st][i]);
+        if (t < rows && sb >= 0) __stcs(reinterpret_cast<uint4 *>(dst + t * pitch), v[st]);
     }
 }
 
+// Grid: x (sequence, new block), y four warps' pieces each.
 template <int ROW, int FMT>
-__global__ void __launch_bounds__(128) evict_copy_kernel(const EvictParams prm) {
+__global__ void __launch_bounds__(128, FMT >= 0 ? 8 : 1) evict_copy_kernel(const EvictParams prm) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the selection
     const int lane = threadIdx.x % 32, Hk = prm.num_kv_heads;
-    const long long item = static_cast<long long>(blockIdx.x) * 4 + threadIdx.x / 32;
-    const int hk = static_cast<int>(item % Hk);
-    const long long bb = item / Hk;
-    const int blk = static_cast<int>(bb % prm.dst_blocks);
-    const long long b = bb / prm.dst_blocks;
-    if (b >= prm.num_seqs) return;
+    const int part = blockIdx.y * 4 + threadIdx.x / 32;
+    if (part >= (FMT >= 0 ? 2 * Hk : Hk)) return;
+    const int hk = part < Hk ? part : part - Hk;
+    const unsigned b = blockIdx.x / static_cast<unsigned>(prm.dst_blocks);
+    const int blk = static_cast<int>(blockIdx.x - b * prm.dst_blocks);
     const int n = clamp_context(__ldg(prm.context_lens + b), evict_cap(prm), false);
     const int rows = min(min(n, prm.keep) - blk * kBlockSize, kBlockSize);
     if (rows <= 0) return;
-    const long long dst = __ldg(prm.dst_tables + b * prm.dst_blocks + blk);
+    const long long dst = __ldg(prm.dst_tables + blockIdx.x);
     // lane t < rows: the entry that row t holds, and its block
     int kept = 0, src = -1;
     if (lane < rows) {
-        kept = __ldcg(prm.kept + (b * Hk + hk) * prm.keep + blk * kBlockSize + lane);
-        src = __ldg(prm.block_tables + b * prm.max_blocks + kept / kBlockSize);
+        kept = __ldcg(prm.kept + (static_cast<size_t>(b) * Hk + hk) * prm.keep + blk * kBlockSize + lane);
+        src = __ldg(prm.block_tables + static_cast<size_t>(b) * prm.max_blocks + kept / kBlockSize);
         if (src < 0 || src >= prm.num_blocks) {
             flag_status(PA_STATUS_BAD_BLOCK_ID);
             src = -1;
@@ -279,8 +404,13 @@ __global__ void __launch_bounds__(128) evict_copy_kernel(const EvictParams prm) 
         if (lane == 0) flag_status(PA_STATUS_BAD_BLOCK_ID);
         return;
     }
-    copy_rows<ROW, FMT>(prm.k_cache, prm.k_scales, kept, rows, src, dst, Hk, hk);
-    copy_rows<ROW, FMT>(prm.v_cache, prm.v_scales, kept, rows, src, dst, Hk, hk);
+    if constexpr (FMT >= 0) {
+        const bool k = part < Hk;
+        copy_rows<ROW, FMT>(k ? prm.k_cache : prm.v_cache, k ? prm.k_scales : prm.v_scales, kept, rows, src, dst, Hk, hk);
+    } else {
+        copy_rows<ROW, FMT>(prm.k_cache, nullptr, kept, rows, src, dst, Hk, hk);
+        copy_rows<ROW, FMT>(prm.v_cache, nullptr, kept, rows, src, dst, Hk, hk);
+    }
 }
 
 }  // namespace pa

@@ -9,6 +9,7 @@ fallback: if libpa.so is missing, importing this module raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -331,6 +332,42 @@ def pa_swap_blocks(dst, src, block_pairs, stream=None) -> None:
 
 
 # ---- rotary positions, the block-scaled 8-bit cache, weight-counting decode, eviction ----
+#
+# These are called once a layer and step, some for kernels of a few microseconds, so the checks are kept short:
+# plain comparisons, data_ptr() as an int, the current stream's handle without a Stream object, and pa_shape structs
+# shared by their values.
+
+
+@functools.lru_cache(maxsize=256)
+def _shape(num_heads, num_kv_heads, head_dim, block_size, num_blocks, dtype, kv_fp8, k_scale=0.0, v_scale=0.0):
+    return PaShape(num_heads=num_heads, num_kv_heads=num_kv_heads, head_dim=head_dim, block_size=block_size,
+                   num_blocks=num_blocks, dtype=dtype, kv_fp8=kv_fp8, k_scale=k_scale, v_scale=v_scale)
+
+
+def _device_of(*tensors) -> int:
+    """The one device of the tensors, which is the current one; all but None are contiguous."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None:
+            if t.get_device() != dev or dev < 0:
+                raise ValueError("all tensors must be on one CUDA device")
+            if not t.is_contiguous():
+                raise ValueError("tensor must be contiguous")
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors are on cuda:%d, which is not the current device" % dev)
+    return dev
+
+
+def _stream_on(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError("the stream and the tensors are on different devices")
+    return stream.cuda_stream
+
+
+def _optional(t):
+    return t.data_ptr() if t is not None else None
 
 
 def pa_rope_init(rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
@@ -346,143 +383,159 @@ def pa_rope_init(rot_dim: int, base: float = 10000.0, interleaved: bool = False,
     return plan
 
 
-def _rows(t: torch.Tensor, name: str, tokens: int, heads: int, dim: int):
-    """Pointer and token stride (elements) of [T, heads, D] rows whose last two dims are contiguous."""
-    if not t.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
-    if t.shape != (tokens, heads, dim):
-        raise ValueError("%s must be [%d, %d, %d], got %s" % (name, tokens, heads, dim, tuple(t.shape)))
+def _row_stride(t: torch.Tensor, dev: int, heads: int, dim: int) -> int:
+    """Token stride (elements) of [T, heads, dim] rows whose last two dims are contiguous."""
+    if t.get_device() != dev:
+        raise ValueError("all tensors must be on one CUDA device")
     stride = t.stride()
-    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
-        raise ValueError("%s must have contiguous heads (any token stride)" % name)
-    return ctypes.c_void_p(t.data_ptr()), (stride[0] if tokens > 1 else heads * dim)
+    if stride[2] != 1 or (stride[1] != dim and heads > 1):
+        raise ValueError("q, k and v rows must have contiguous heads (any token stride)")
+    return stride[0] if t.shape[0] > 1 else heads * dim
 
 
 def pa_rope(q_out, k_out, q, k, positions, plan: PaRopePlan, stream=None) -> None:
     """Rotate q [T, H, D] and k [T, Hk, D] by position (token strides are free; in place where contiguous)."""
-    _same_dtype(q_out, k_out, q, k)
+    dt = q.dtype
+    if k.dtype != dt or q_out.dtype != dt or k_out.dtype != dt:
+        raise ValueError("q, k and their outputs must share one dtype")
     _int(positions, torch.int64, "positions")
     T, H, D = q.shape
     Hk = k.shape[1]
-    if q_out.shape != q.shape or k_out.shape != k.shape or positions.shape != (T,):
+    if q_out.shape != q.shape or k.shape != (T, Hk, D) or k_out.shape != k.shape or positions.shape != (T,):
         raise ValueError("q, q_out [T, H, D]; k, k_out [T, Hk, D]; positions [T]")
-    qp, qs = _rows(q, "q", T, H, D)
-    kp, ks = _rows(k, "k", T, Hk, D)
-    shape = PaShape(num_heads=H, num_kv_heads=Hk, head_dim=D, block_size=BLOCK_SIZE, num_blocks=1,
-                    dtype=_dtype_code(q.dtype))
-    _check("pa_rope", lib.pa_rope(_ptr(q_out), _ptr(k_out), qp, kp, qs, ks, _ptr(positions), T, ctypes.byref(plan),
-                                  ctypes.byref(shape), _stream(stream)))
+    dev = _device_of(q_out, k_out, positions)
+    shape = _shape(H, Hk, D, BLOCK_SIZE, 1, _dtype_code(dt), 0)
+    _check("pa_rope", lib.pa_rope(q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+                                  _row_stride(q, dev, H, D), _row_stride(k, dev, Hk, D), positions.data_ptr(), T,
+                                  plan, shape, _stream_on(stream, dev)))
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, plan: PaRopePlan, stream=None,
                       k_scale: float = 0.0, v_scale: float = 0.0) -> None:
     """Rotate q [T, H, D] into q_out, and write the rotated k and v [T, Hk, D] to their slots of the pool."""
-    _same_dtype_kv((q_out, q, k, v), (k_cache, v_cache))
+    dt = q.dtype
+    if q_out.dtype != dt or k.dtype != dt or v.dtype != dt:
+        raise ValueError("q, q_out, k and v must share one dtype")
     _int(slot_mapping, torch.int64, "slot_mapping")
     _int(positions, torch.int64, "positions")
     T, H, D = q.shape
-    shape = shape_of(k_cache, H, k_scale, v_scale)
+    shape = _pool_shape(k_cache, v_cache, H, D, dt, k_scale, v_scale, None, None)
     Hk = shape.num_kv_heads
-    if (q_out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[3] != D
-            or positions.shape != (T,) or slot_mapping.shape != (T,)):
-        raise ValueError("q, q_out [T, H, D]; caches [NB, 16, Hk, D]; slot_mapping, positions [T]")
-    qp, qs = _rows(q, "q", T, H, D)
-    kp, ks = _rows(k, "k", T, Hk, D)
-    vp, vs = _rows(v, "v", T, Hk, D)
+    rows = (T, Hk, D)
+    if (q_out.shape != q.shape or k.shape != rows or v.shape != rows or positions.shape != (T,)
+            or slot_mapping.shape != (T,)):
+        raise ValueError("q, q_out [T, H, D]; k, v [T, Hk, D]; slot_mapping, positions [T]")
+    dev = _device_of(q_out, k_cache, v_cache, slot_mapping, positions)
     _check("pa_rope_and_cache",
-           lib.pa_rope_and_cache(_ptr(q_out), qp, kp, vp, qs, ks, vs, _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(slot_mapping), _ptr(positions), T, ctypes.byref(plan), ctypes.byref(shape),
-                                 _stream(stream)))
+           lib.pa_rope_and_cache(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                 _row_stride(q, dev, H, D), _row_stride(k, dev, Hk, D), _row_stride(v, dev, Hk, D),
+                                 k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+                                 positions.data_ptr(), T, plan, shape, _stream_on(stream, dev)))
 
 
 def shape_of_block8(k_codes: torch.Tensor, num_heads: int) -> PaShape:
     """pa_shape of a block8 pool [NB, 16, Hk, D]: uint8 E4M3 codes or int8 codes, beside bf16 q and out."""
+    return PaShape.from_buffer_copy(_codes_shape(k_codes, num_heads))
+
+
+def _codes_shape(k_codes: torch.Tensor, num_heads: int) -> PaShape:
     if k_codes.dim() != 4:
         raise ValueError("codes must be [num_blocks, block_size, num_kv_heads, head_dim]")
-    if k_codes.dtype not in (torch.uint8, torch.int8):
-        raise ValueError("block8 codes are uint8 (E4M3) or int8, got %s" % k_codes.dtype)
+    dt = k_codes.dtype
+    if dt != torch.uint8 and dt != torch.int8:
+        raise ValueError("block8 codes are uint8 (E4M3) or int8, got %s" % dt)
     nb, bs, hk, d = k_codes.shape
-    return PaShape(num_heads=int(num_heads), num_kv_heads=hk, head_dim=d, block_size=bs, num_blocks=nb,
-                   dtype=PA_DTYPE_BF16,
-                   kv_fp8=PA_KV_BLOCK_E4M3 if k_codes.dtype == torch.uint8 else PA_KV_BLOCK_INT8)
+    return _shape(int(num_heads), hk, d, bs, nb, PA_DTYPE_BF16,
+                  PA_KV_BLOCK_E4M3 if dt == torch.uint8 else PA_KV_BLOCK_INT8)
 
 
-def _check_block8(k_codes, v_codes, k_scales, v_scales):
-    if v_codes.shape != k_codes.shape or v_codes.dtype != k_codes.dtype:
+def _block8_shape(k_codes, v_codes, k_scales, v_scales, num_heads) -> PaShape:
+    shape = _codes_shape(k_codes, num_heads)
+    if v_codes.dtype != k_codes.dtype or v_codes.shape != k_codes.shape:
         raise ValueError("k_codes and v_codes must have one shape and dtype")
-    want = (k_codes.shape[0], k_codes.shape[2])
-    for t in (k_scales, v_scales):
-        if t.dtype != torch.float32 or t.shape != want:
-            raise ValueError("scales must be float32 [num_blocks, num_kv_heads]")
+    want = (shape.num_blocks, shape.num_kv_heads)
+    if (k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32 or k_scales.shape != want
+            or v_scales.shape != want):
+        raise ValueError("scales must be float32 [num_blocks, num_kv_heads]")
+    return shape
 
 
-def _pool_shape(k_cache, v_cache, num_heads, k_scale, v_scale, k_scales, v_scales) -> PaShape:
-    """The shape of a plain pool, or of a block8 pool where its scales are given."""
-    if (k_scales is None) != (v_scales is None):
-        raise ValueError("give both k_scales and v_scales, or neither")
-    if k_scales is not None:
-        _check_block8(k_cache, v_cache, k_scales, v_scales)
-        return shape_of_block8(k_cache, num_heads)
-    _same_dtype(k_cache, v_cache)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape")
-    return shape_of(k_cache, num_heads, k_scale, v_scale)
+def _pool_shape(k_cache, v_cache, num_heads, head_dim, dtype, k_scale, v_scale, k_scales, v_scales) -> PaShape:
+    """The shape of a pool read or written next to q of `dtype`: a block8 pool where its scales are given."""
+    if k_scales is not None or v_scales is not None:
+        if k_scales is None or v_scales is None:
+            raise ValueError("give both k_scales and v_scales, or neither")
+        shape = _block8_shape(k_cache, v_cache, k_scales, v_scales, num_heads)
+        fp8 = True
+    else:
+        if k_cache.dim() != 4:
+            raise ValueError("k_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
+        if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
+            raise ValueError("k_cache and v_cache must have one shape and dtype")
+        nb, bs, hk, d = k_cache.shape
+        fp8 = k_cache.dtype == torch.uint8
+        shape = _shape(int(num_heads), hk, d, bs, nb, PA_DTYPE_BF16 if fp8 else _dtype_code(k_cache.dtype),
+                       1 if fp8 else 0, float(k_scale), float(v_scale))
+    if dtype != (torch.bfloat16 if fp8 else k_cache.dtype):
+        raise ValueError("q, out and new tokens must have the pool's dtype (bf16 beside 8-bit pools)")
+    if shape.head_dim != head_dim:
+        raise ValueError("q and the pool must have one head_dim")
+    return shape
 
 
 def pa_cache_block8(k, v, k_codes, v_codes, k_scales, v_scales, slot_mapping, stream=None) -> None:
     """Append new tokens' bf16 K/V rows to a block8 pool; the tokens of one block are neighbours in the call."""
-    shape = shape_of_block8(k_codes, k_codes.shape[2])
-    _check_block8(k_codes, v_codes, k_scales, v_scales)
+    shape = _block8_shape(k_codes, v_codes, k_scales, v_scales, k_codes.shape[2])
     _int(k, torch.bfloat16, "k")
     _int(v, torch.bfloat16, "v")
     _int(slot_mapping, torch.int64, "slot_mapping")
-    if k.shape[1:] != k_codes.shape[2:] or v.shape != k.shape or slot_mapping.shape != (k.shape[0],):
+    T = k.shape[0]
+    rows = (T, shape.num_kv_heads, shape.head_dim)
+    if k.shape != rows or v.shape != rows or slot_mapping.shape != (T,):
         raise ValueError("k, v must be [T, Hk, D] matching the pool; slot_mapping [T]")
+    dev = _device_of(k, v, k_codes, v_codes, k_scales, v_scales, slot_mapping)
     _check("pa_cache_block8",
-           lib.pa_cache_block8(_ptr(k), _ptr(v), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales),
-                               _ptr(slot_mapping), k.shape[0], ctypes.byref(shape), _stream(stream)))
+           lib.pa_cache_block8(k.data_ptr(), v.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
+                               k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, shape,
+                               _stream_on(stream, dev)))
 
 
 def pa_decode_block8_workspace_bytes(num_seqs: int, max_context_len: int, partition_tokens: int,
                                      shape: PaShape) -> int:
-    n = lib.pa_decode_block8_workspace_bytes(int(num_seqs), int(max_context_len), int(partition_tokens),
-                                             ctypes.byref(shape))
+    n = lib.pa_decode_block8_workspace_bytes(int(num_seqs), int(max_context_len), int(partition_tokens), shape)
     if n < 0:
         raise PaError("pa_decode_block8_workspace_bytes", int(n))
     return int(n)
 
 
-def _check_decode(out, q, k_cache, block_tables, context_lens):
+def _check_decode(out, q, block_tables, context_lens):
     _int(block_tables, torch.int32, "block_tables")
     _int(context_lens, torch.int32, "context_lens")
-    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
-        raise ValueError("q must be [B, H, D] with the pool's D")
     B = q.shape[0]
-    if out.shape != q.shape or block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
-        raise ValueError("q, out [B, H, D]; block_tables [B, MB]; context_lens [B]")
+    if (out.dtype != q.dtype or q.dim() != 3 or out.shape != q.shape or block_tables.dim() != 2
+            or block_tables.shape[0] != B or context_lens.shape != (B,)):
+        raise ValueError("q, out [B, H, D] of one dtype; block_tables [B, MB]; context_lens [B]")
 
 
 def pa_decode_block8(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens, max_context_len: int,
                      scale: float, partition_tokens: int = 0, workspace: Optional[torch.Tensor] = None,
                      stream=None) -> None:
     """pa_decode over a block8 pool: uint8 (E4M3) or int8 codes with fp32 scales [NB, Hk]."""
-    _check_block8(k_codes, v_codes, k_scales, v_scales)
-    _int(q, torch.bfloat16, "q")
-    _int(out, torch.bfloat16, "out")
-    _check_decode(out, q, k_codes, block_tables, context_lens)
-    shape = shape_of_block8(k_codes, q.shape[1])
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check_decode(out, q, block_tables, context_lens)
+    B, H, D = q.shape
+    shape = _pool_shape(k_codes, v_codes, H, D, q.dtype, 0.0, 0.0, k_scales, v_scales)
+    dev = _device_of(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens, workspace)
     _check("pa_decode_block8",
-           lib.pa_decode_block8(_ptr(out), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales),
-                                _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), q.shape[0],
-                                int(max_context_len), float(scale), int(partition_tokens), _ptr(workspace), ws_bytes,
-                                ctypes.byref(shape), _stream(stream)))
+           lib.pa_decode_block8(out.data_ptr(), q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
+                                k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+                                block_tables.shape[1], context_lens.data_ptr(), B, int(max_context_len), float(scale),
+                                int(partition_tokens), _optional(workspace),
+                                workspace.nbytes if workspace is not None else 0, shape, _stream_on(stream, dev)))
 
 
 def pa_decode_weights_workspace_bytes(num_seqs: int, max_context_len: int, partition_tokens: int,
                                       shape: PaShape) -> int:
-    n = lib.pa_decode_weights_workspace_bytes(int(num_seqs), int(max_context_len), int(partition_tokens),
-                                              ctypes.byref(shape))
+    n = lib.pa_decode_weights_workspace_bytes(int(num_seqs), int(max_context_len), int(partition_tokens), shape)
     if n < 0:
         raise PaError("pa_decode_weights_workspace_bytes", int(n))
     return int(n)
@@ -496,21 +549,19 @@ def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_l
 
     A pool with k_scales and v_scales [NB, Hk] is a block8 pool; a uint8 pool without them takes k_scale, v_scale.
     """
-    _same_dtype(out, q)
-    _check_decode(out, q, k_cache, block_tables, context_lens)
+    _check_decode(out, q, block_tables, context_lens)
     _int(weights, torch.float32, "weights")
-    shape = _pool_shape(k_cache, v_cache, q.shape[1], k_scale, v_scale, k_scales, v_scales)
-    if _dtype_code(q.dtype) != shape.dtype:
-        raise ValueError("q and out must have the pool's dtype (bf16 beside 8-bit pools)")
-    if weights.dim() != 3 or weights.shape[:2] != (q.shape[0], shape.num_kv_heads):
+    B, H, D = q.shape
+    shape = _pool_shape(k_cache, v_cache, H, D, q.dtype, k_scale, v_scale, k_scales, v_scales)
+    if weights.dim() != 3 or weights.shape[0] != B or weights.shape[1] != shape.num_kv_heads:
         raise ValueError("weights must be [B, Hk, W]")
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    dev = _device_of(out, weights, q, k_cache, v_cache, block_tables, context_lens, workspace, k_scales, v_scales)
     _check("pa_decode_weights",
-           lib.pa_decode_weights(_ptr(out), _ptr(weights), weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), block_tables.shape[1],
-                                 _ptr(context_lens), q.shape[0], int(max_context_len), float(scale),
-                                 int(partition_tokens), _ptr(workspace), ws_bytes, ctypes.byref(shape),
-                                 _stream(stream)))
+           lib.pa_decode_weights(out.data_ptr(), weights.data_ptr(), weights.shape[2], q.data_ptr(),
+                                 k_cache.data_ptr(), v_cache.data_ptr(), _optional(k_scales), _optional(v_scales),
+                                 block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B,
+                                 int(max_context_len), float(scale), int(partition_tokens), _optional(workspace),
+                                 workspace.nbytes if workspace is not None else 0, shape, _stream_on(stream, dev)))
 
 
 def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, dst_block_tables, new_weights, new_context_lens,
@@ -521,7 +572,11 @@ def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, dst_block_ta
     kept int32 [B, Hk, keep], new_weights float32 [B, Hk, 16 * dst_block_tables.shape[1]] and new_context_lens
     int32 [B] are written; the old blocks, tables, lengths and weights are only read.
     """
-    shape = _pool_shape(k_cache, v_cache, k_cache.shape[2], 1.0, 1.0, k_scales, v_scales)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
+    plain = k_scales is None and k_cache.dtype != torch.uint8
+    shape = _pool_shape(k_cache, v_cache, k_cache.shape[2], k_cache.shape[3],
+                        k_cache.dtype if plain else torch.bfloat16, 1.0, 1.0, k_scales, v_scales)
     for t, name in ((block_tables, "block_tables"), (context_lens, "context_lens"),
                     (dst_block_tables, "dst_block_tables"), (new_context_lens, "new_context_lens"), (kept, "kept")):
         _int(t, torch.int32, name)
@@ -534,12 +589,15 @@ def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, dst_block_ta
             or new_weights.shape != (B, Hk, dst_block_tables.shape[1] * BLOCK_SIZE)):
         raise ValueError("context_lens, new_context_lens [B]; block_tables, dst_block_tables [B, .]; weights, kept "
                          "[B, Hk, .]; new_weights [B, Hk, 16 * dst blocks]")
+    dev = _device_of(k_cache, v_cache, weights, block_tables, context_lens, dst_block_tables, new_weights,
+                     new_context_lens, kept, k_scales, v_scales)
     _check("pa_evict",
-           lib.pa_evict(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), _ptr(weights),
-                        weights.shape[2], _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-                        _ptr(dst_block_tables), dst_block_tables.shape[1], _ptr(new_weights), _ptr(new_context_lens),
-                        _ptr(kept), B, int(max_context_len), kept.shape[2], int(sinks), int(recent),
-                        ctypes.byref(shape), _stream(stream)))
+           lib.pa_evict(k_cache.data_ptr(), v_cache.data_ptr(), _optional(k_scales), _optional(v_scales),
+                        weights.data_ptr(), weights.shape[2], block_tables.data_ptr(), block_tables.shape[1],
+                        context_lens.data_ptr(), dst_block_tables.data_ptr(), dst_block_tables.shape[1],
+                        new_weights.data_ptr(), new_context_lens.data_ptr(), kept.data_ptr(), B,
+                        int(max_context_len), kept.shape[2], int(sinks), int(recent), shape,
+                        _stream_on(stream, dev)))
 
 
 def pa_get_status(stream=None) -> int:
