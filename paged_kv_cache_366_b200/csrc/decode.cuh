@@ -189,6 +189,8 @@ struct DecodeParams {
     int max_blocks_per_seq;
     int num_heads;
     int num_kv_heads;
+    int list_heads;    // heads, or groups of `share` heads that one slice streams together, of the work list
+    int share;         // KV heads of one list entry: num_kv_heads = list_heads * share
     int max_context_len;
     float scale_log2;  // softmax scale * log2(e) (times k_scale for an FP8 cache)
     float v_scale;     // 1, or the FP8 value scale
@@ -200,7 +202,7 @@ struct DecodeParams {
 // Position in the flat (sequence, KV head, block) list.
 struct Cursor {
     int r;      // flat index minus the slice's first index
-    int b, hk;  // the unit
+    int b, hk;  // the unit (hk: the KV head, or group of heads)
     int c;      // context length of b (clamped)
     int nblk;   // blocks of the unit
     int blk;    // block within the unit
@@ -219,7 +221,7 @@ __device__ __forceinline__ int cursor_advance(Cursor &x, int n, const DecodePara
     while (x.blk >= x.nblk) {
         x.blk -= x.nblk;
         ++passed;
-        if (++x.hk == prm.num_kv_heads) {
+        if (++x.hk == prm.list_heads) {
             x.hk = 0;
             do {
                 if (++x.b >= prm.num_seqs) {  // past the end of the list: never used for a block
@@ -240,17 +242,16 @@ __device__ __forceinline__ int slice_of(long long f, long long N, int W) {
     return static_cast<int>(((f + 1) * W - 1) / N);
 }
 
-// The start of a decode CTA of WARPS warps (the whole CTA takes part): the
-// list's block count N, its number of slices WS, and for each warp the first
-// block of its slice in `starts` (5 ints: b, hk, blk, c, nblk). Rows of
-// sequences of length 0 are written as zeros here. `cum` is CHUNK entries of
-// shared memory, free again on return.
-template <typename Tq, int D, int WARPS, int CHUNK>
-__device__ __forceinline__ void decode_prologue(const DecodeParams &prm, long long *cum, int *starts, long long &N,
-                                                int &WS) {
-    constexpr int THREADS = 32 * WARPS;
+// The start of a decode CTA of THREADS threads, all of which take part, and
+// `own` slices (at most THREADS): the list's block count N, its number of slices
+// WS, and for each slice of the CTA its first block in `starts` (5 ints: b, hk,
+// blk, c, nblk). Rows of sequences of length 0 are written as zeros here. `cum`
+// is CHUNK entries of shared memory, free again on return.
+template <typename Tq, int D, int CHUNK, int THREADS>
+__device__ __forceinline__ void decode_prologue(const DecodeParams &prm, long long *cum, int *starts, int own,
+                                                long long &N, int &WS) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int B = prm.num_seqs, Hk = prm.num_kv_heads;
+    const int B = prm.num_seqs, Hk = prm.list_heads;
     const int cap = decode_cap(prm);
     // While the prologue scans the lengths, bring the block tables towards L2
     // (each CTA a 1/gridDim share, 128-byte lines), so that a warp's first
@@ -282,11 +283,11 @@ __device__ __forceinline__ void decode_prologue(const DecodeParams &prm, long lo
         if (lane == 0) cum[warp] = part;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) N += cum[w];
+        for (int w = 0; w < THREADS / 32; ++w) N += cum[w];
         N *= Hk;
         __syncthreads();
     }
-    const int cta0 = static_cast<int>(blockIdx.x) * WARPS;  // first slice of this CTA
+    const int cta0 = static_cast<int>(blockIdx.x) * own;  // first slice of this CTA
     WS = 0;  // slices: at most one per block, so that none is empty (a unit's slices are then
              // exactly those from the slice of its first block to that of its last)
     {
@@ -314,7 +315,7 @@ __device__ __forceinline__ void decode_prologue(const DecodeParams &prm, long lo
             }
             __syncthreads();
             if (B <= CHUNK) N = cum[n - 1];  // one chunk: the total comes with the scan
-            WS = static_cast<int>(min(static_cast<long long>(gridDim.x) * WARPS, N));
+            WS = static_cast<int>(min(static_cast<long long>(gridDim.x) * own, N));
             // a sequence of length 0 has no blocks: CTA b % gridDim.x writes its zero rows
             for (int i = threadIdx.x; i < n; i += THREADS) {
                 const long long hi = cum[i], lo = i ? cum[i - 1] : base;
@@ -326,7 +327,7 @@ __device__ __forceinline__ void decode_prologue(const DecodeParams &prm, long lo
             }
             // thread w: the first block of slice cta0 + w, if it lies in this chunk
             const int w = threadIdx.x;
-            if (w < WARPS && cta0 + w < WS) {
+            if (w < own && cta0 + w < WS) {
                 const long long f = N * (cta0 + w) / WS;
                 if (f >= base && f < cum[n - 1]) {
                     int lo_i = 0, hi_i = n - 1;  // the first sequence whose inclusive sum exceeds f
@@ -398,7 +399,8 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     long long N;
     int WS;  // slices: at most one per block
-    decode_prologue<Tq, D, C::WARPS, C::RING_BYTES / 8>(prm, reinterpret_cast<long long *>(smem), starts, N, WS);
+    decode_prologue<Tq, D, C::RING_BYTES / 8, C::THREADS>(prm, reinterpret_cast<long long *>(smem), starts, C::WARPS, N,
+                                                          WS);
     const int cta0 = static_cast<int>(blockIdx.x) * C::WARPS;  // first slice of this CTA
     if (cta0 >= WS) return;
     // ---- from here on every warp runs alone on its slice
@@ -781,7 +783,8 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
 
 // Merge the partials of every unit cut by slice boundaries:
 //   M = max_s m_s,  L = sum_s 2^(m_s - M) l_s,  out = sum_s 2^(m_s - M) O_s / L
-// over the unit's slices s (slots first + u .. first + slices - 1 + u). Grid
+// over the unit's slices s (slots first + u .. first + slices - 1 + u; where a list
+// entry is `share` heads, each slot holds theirs one after another). Grid
 // (units, G*D/128 column groups) of MG warps: a lane takes four consecutive
 // columns of one head, warp w the slices w, w + MG, ... with every slot's
 // loads of a round in flight together (up to 8 slots a round); with MG > 1,
@@ -799,6 +802,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
     __shared__ float sh_m[MG][32], sh_l[MG][32];
     const int u = blockIdx.x;
     const int b = u / prm.num_kv_heads, hk = u % prm.num_kv_heads;
+    const int lu = u / prm.share;  // the list's unit: share divides num_kv_heads
     const int lane = threadIdx.x % 32, grp = threadIdx.x / 32;
     const int idx = 4 * (blockIdx.y * 32 + lane);
     const bool col = idx < G * D;  // the same for every warp: lanes past G * D only take part in the barrier
@@ -813,7 +817,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         long long below = 0, total = 0;
         for (int i = lane; i < prm.num_seqs; i += 32) {
             const int c = clamp_context(__ldg(prm.context_lens + i), cap, false);
-            const long long n = static_cast<long long>((c + kBlockSize - 1) / kBlockSize) * prm.num_kv_heads;
+            const long long n = static_cast<long long>((c + kBlockSize - 1) / kBlockSize) * prm.list_heads;
             total += n;
             below += i < b ? n : 0;
         }
@@ -823,7 +827,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
             below += __shfl_xor_sync(0xffffffffu, below, off);
         }
         const int nblk = (c_b + kBlockSize - 1) / kBlockSize;
-        const long long u_lo = below + static_cast<long long>(hk) * nblk;
+        const long long u_lo = below + static_cast<long long>(hk / prm.share) * nblk;
         const int ws = static_cast<int>(min(static_cast<long long>(prm.warps_total), total));
         first = slice_of(u_lo, total, ws);
         nseg = slice_of(u_lo + nblk - 1, total, ws) - first + 1;
@@ -831,12 +835,12 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         asm volatile("griddepcontrol.wait;" ::: "memory");
     } else {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        first = __ldcg(prm.ws_unit + 2 * u);
-        nseg = __ldcg(prm.ws_unit + 2 * u + 1);
+        first = __ldcg(prm.ws_unit + 2 * lu);
+        nseg = __ldcg(prm.ws_unit + 2 * lu + 1);
         if (nseg <= 1) return;  // a whole unit: written by the decode kernel
     }
     const int g = col ? idx / D : 0, d = col ? idx % D : 0;
-    const int s0 = first + u;
+    const int s0 = first + lu;
     float M = -CUDART_INF_F, Lsum = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = grp; p0 < nseg; p0 += 8 * MG) {
@@ -846,7 +850,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         for (int i = 0; i < 8; ++i) {
             const int p = p0 + i * MG;
             const bool in = col && p < nseg;
-            const size_t s = static_cast<size_t>(s0 + p);
+            const size_t s = static_cast<size_t>(s0 + p) * prm.share + (hk - hk / prm.share * prm.share);
             mp[i] = in ? __ldcg(prm.ws_m + s * G + g) : -CUDART_INF_F;
             lp[i] = in ? __ldcg(prm.ws_l + s * G + g) : 0.f;
             op[i] = in ? __ldcg(reinterpret_cast<const float4 *>(prm.ws_o + (s * G + g) * D + d))

@@ -4,8 +4,11 @@
 //   K[p] = k_codes[block][p % 16] * k_scales[block][hk], V likewise,
 //   block = block_tables[b][p / 16].
 //
-// The work list, its slices, the partials and the merge are decode_kernel's. What
-// differs is the block step, because the bytes are half of a bf16 cache's: at the
+// The work list, its slices, the partials and the merge are decode_kernel's, with up to
+// four neighbouring KV heads to a list entry, which as many warps take from one stage:
+// the heads' rows of a token are neighbours in memory, and 128-byte pieces of them at
+// far apart times stream at 5.1 TB/s where four together PLACEHOLDER. What differs
+// beside that is the block step, because the bytes are half of a bf16 cache's: at the
 // copy bandwidth an SM has about 180 cycles for a block of one KV head, and the
 // packed-FMA step of decode_kernel takes over 750 issue slots. So here a block is two
 // small matrix products on the warp's tensor instructions (m16n8k16, f16 operands,
@@ -45,21 +48,30 @@ struct Block8Params {
     const float *k_scales, *v_scales;  // [NB][Hk]
 };
 
-template <int D, int G>
+// A CTA is WARPS consumer warps and a producer warp. `share` consumer warps (4, 2 or 1:
+// the most that divide the KV heads) form a group that streams one slice, a KV head each:
+// a stage is one block's K and V tiles of `share` neighbouring heads.
+template <int D>
 struct Block8Cfg {
-    static constexpr int STAGE_BYTES = 2 * kBlockSize * D;  // K and V codes of one block of one KV head
+    static constexpr int TILE = kBlockSize * D;      // codes of one block of one KV head, K or V
     static constexpr int WARPS = 12;
-    static constexpr int NSTAGE = D == 128 ? 4 : 8;  // 16 KB in flight per warp
-    static constexpr int THREADS = 32 * WARPS;
-    static constexpr int WARP_RING = NSTAGE * STAGE_BYTES;
-    static constexpr int RING_BYTES = WARPS * WARP_RING;
-    static constexpr int OFF_BAR = RING_BYTES;
-    static constexpr int OFF_SCALE = OFF_BAR + WARPS * NSTAGE * 8;  // per stage: k_scale, v_scale
-    static constexpr int OFF_MISC = OFF_SCALE + WARPS * NSTAGE * 8;
+    static constexpr int NSTAGE = D == 128 ? 4 : 8;  // 16 KB in flight per consumer warp
+    static constexpr int THREADS = 32 * (WARPS + 1);
+    static constexpr int RING_BYTES = WARPS * NSTAGE * 2 * TILE;
+    // per group (at most WARPS) and stage; the scales per warp and stage
+    static constexpr int OFF_META = RING_BYTES;                       // a StageMeta
+    static constexpr int OFF_SCALE = OFF_META + WARPS * NSTAGE * 16;  // k_scale, v_scale
+    static constexpr int OFF_FULL = OFF_SCALE + WARPS * NSTAGE * 8;   // an mbarrier
+    static constexpr int OFF_EMPTY = OFF_FULL + WARPS * NSTAGE * 8;
+    static constexpr int OFF_MISC = OFF_EMPTY + WARPS * NSTAGE * 8;
     static constexpr int SMEM = OFF_MISC + WARPS * 5 * 4 + 16;
-    static_assert(SMEM <= kCtaSmem, "one CTA must fit an SM");
-    static_assert(STAGE_BYTES / 2 % 1024 == 0, "each tile starts on a swizzle period");
+    static_assert(SMEM <= kCtaSmem && WARPS % 4 == 0 && WARPS <= 32, "one CTA must fit an SM, a lane each group");
+    static_assert(TILE % 1024 == 0, "each tile starts on a swizzle period");
 };
+
+// What a stage holds, as one int4: the list's unit, its block, valid rows (0: a bad
+// table entry) with flags.
+constexpr int kMetaFirst = 0x100, kMetaLast = 0x200, kMetaWhole = 0x400, kMetaRows = 0xff;
 
 // d += a b, a [16][16] (row-major fragments), b [16][8], f16 in, fp32 out.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -104,11 +116,134 @@ __device__ __forceinline__ uint32_t tile_at(int t, int c) {
     return t * D + ((D == 128 ? c ^ (t & 7) : c ^ ((t >> 1) & 3)) << 4);
 }
 
+// Non-blocking: whether phase `parity` of an mbarrier has completed.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The producer warp: lane g walks the slice of group g, a few blocks ahead of its
+// consumers. For every block it writes what they need to know, and sends the heads' K
+// and V (two TMA boxes of `share` tiles) and scales (4-byte cp.async each) on the stage's
+// full barrier.
+template <int D>
+__device__ __forceinline__ void block8_produce(const Block8Params &b8, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
+                                               unsigned char *smem, const int *starts, long long N, int WS) {
+    using C = Block8Cfg<D>;
+    const DecodeParams &prm = b8.d;
+    const int g = threadIdx.x % 32, share = prm.share, groups = C::WARPS / share;
+    const int slice = static_cast<int>(blockIdx.x) * groups + g;
+    const bool mine = g < groups && slice < WS;
+    const long long s_lo = mine ? N * slice / WS : 0, s_hi = mine ? N * (slice + 1) / WS : 0;
+    const int nb = static_cast<int>(s_hi - s_lo);
+    Cursor cc{0, 0, 0, 0, 1, 0};
+    if (mine) cc = Cursor{0, starts[5 * g], starts[5 * g + 1], starts[5 * g + 3], starts[5 * g + 4], starts[5 * g + 2]};
+    const uint32_t tiles = share * C::TILE;  // bytes of one TMA box
+    const uint32_t ring = smem_addr(smem) + g * C::NSTAGE * 2 * tiles;
+    int4 *meta = reinterpret_cast<int4 *>(smem + C::OFF_META) + g * C::NSTAGE;
+    const uint32_t scales = smem_addr(smem + C::OFF_SCALE) + g * share * C::NSTAGE * 8;
+    const uint32_t full = smem_addr(smem + C::OFF_FULL) + g * C::NSTAGE * 8;
+    const uint32_t empty = smem_addr(smem + C::OFF_EMPTY) + g * C::NSTAGE * 8;
+    const uint64_t pol = policy_evict_normal();
+
+    // table entries qbase .. qbase + 3 of the unit, and the four after them
+    int qbase = 0, cur[4], nxt[4];
+    auto entries = [&](int (&q)[4], int at) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q[i] = at + i < min(cc.nblk, prm.max_blocks_per_seq)
+                       ? __ldg(prm.block_tables + static_cast<size_t>(cc.b) * prm.max_blocks_per_seq + at + i)
+                       : -1;
+    };
+    auto restart = [&]() {
+        qbase = cc.blk;
+        entries(cur, qbase);
+        entries(nxt, qbase + 4);
+    };
+    if (mine) restart();
+
+    int k = 0, s = 0;          // the next block, its stage
+    uint32_t phase = 1;        // the parity of the stage's last release
+    unsigned long long idle_since = 0;
+    while (true) {
+        const bool todo = k < nb;
+        if (!__any_sync(0xffffffffu, todo)) break;
+        const bool go = todo && (k < C::NSTAGE || mbar_test(empty + 8 * s, phase));
+        if (!__any_sync(0xffffffffu, go)) {
+            const unsigned long long now = global_ns();
+            if (idle_since == 0) idle_since = now;
+            if (now - idle_since > kWaitLimitNs) {  // a consumer gave up: its status says why
+                flag_status(PA_STATUS_WAIT_TIMEOUT);
+                break;
+            }
+            __nanosleep(20);
+            continue;
+        }
+        idle_since = 0;
+        if (go) {
+            const int i = cc.blk - qbase;
+            int pb = i == 0 ? cur[0] : i == 1 ? cur[1] : i == 2 ? cur[2] : cur[3];
+            int rows = cc.blk == cc.nblk - 1 ? cc.c - cc.blk * kBlockSize : kBlockSize;
+            if (pb < 0 || pb >= prm.num_blocks) {
+                flag_status(PA_STATUS_BAD_BLOCK_ID);
+                pb = 0;
+                rows = 0;
+            }
+            const int u = cc.b * prm.list_heads + cc.hk;
+            const long long u_lo = s_lo + k - cc.blk, u_hi = u_lo + cc.nblk;  // the unit's positions in the list
+            const bool whole = u_lo >= s_lo && u_hi <= s_hi;
+            const bool last = cc.blk == cc.nblk - 1 || k == nb - 1;
+            meta[s] = make_int4(u, cc.blk,
+                                rows | (cc.blk == 0 || k == 0 ? kMetaFirst : 0) | (last ? kMetaLast : 0) |
+                                    (whole ? kMetaWhole : 0),
+                                0);
+            const uint32_t bar = full + 8 * s, dst = ring + s * 2 * tiles;
+            const int head = cc.hk * share;
+            mbar_arrive_expect_tx(bar, 2 * tiles);
+            tma_load_3d_policy(dst, tm_k, 0, pb * kBlockSize, head, bar, pol);
+            tma_load_3d_policy(dst + tiles, tm_v, 0, pb * kBlockSize, head, bar, pol);
+            const size_t at = static_cast<size_t>(pb) * prm.num_kv_heads + head;
+            for (int h = 0; h < share; ++h) {
+                cp_async4(scales + (h * C::NSTAGE + s) * 8, b8.k_scales + at + h);
+                cp_async4(scales + (h * C::NSTAGE + s) * 8 + 4, b8.v_scales + at + h);
+            }
+            cp_async_arrive(bar);
+            if (cc.blk == 0) {  // where the unit's partials are
+                int *rec = prm.ws_unit + 2 * static_cast<size_t>(u);
+                rec[0] = slice;
+                rec[1] = whole ? 1 : slice_of(u_hi - 1, N, WS) - slice + 1;
+            }
+            if (++s == C::NSTAGE) {
+                s = 0;
+                phase ^= 1;
+            }
+            if (++k < nb) {
+                if (cursor_advance(cc, 1, prm) > 0) {
+                    restart();
+                } else if (cc.blk == qbase + 4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) cur[j] = nxt[j];
+                    qbase += 4;
+                    entries(nxt, qbase + 4);
+                }
+            }
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 template <int FMT, int D, int G, bool EMIT>
-__global__ void __launch_bounds__(Block8Cfg<D, G>::THREADS, 1)
-    decode_block8_kernel(const Block8Params b8, const __grid_constant__ CUtensorMap tm_k,
+__global__ void __launch_bounds__(Block8Cfg<D>::THREADS, 1)
+    decode_block8_kernel(const __grid_constant__ Block8Params b8, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v) {
-    using C = Block8Cfg<D, G>;
+    using C = Block8Cfg<D>;
     using T = __nv_bfloat16;
     constexpr int KC = D / 64;     // 16-code chunks of a K row per lane
     constexpr int VW = D / 32;     // 4-code words of a V row per lane
@@ -116,87 +251,47 @@ __global__ void __launch_bounds__(Block8Cfg<D, G>::THREADS, 1)
     const DecodeParams &prm = b8.d;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int gid = lane / 4, tid = lane % 4;
-    const int Hk = prm.num_kv_heads;
 
     extern __shared__ __align__(1024) unsigned char smem_b8[];
     int *starts = reinterpret_cast<int *>(smem_b8 + C::OFF_MISC);
+    const int share = prm.share, group = warp / share, sub = warp - group * share;  // sub: the head of the group
+    const uint32_t full = smem_addr(smem_b8 + C::OFF_FULL) + group * C::NSTAGE * 8;
+    const uint32_t empty = smem_addr(smem_b8 + C::OFF_EMPTY) + group * C::NSTAGE * 8;
+    if (warp < C::WARPS && sub == 0 && lane < C::NSTAGE) {
+        mbar_init(full + 8 * lane, 2);       // the producer lane: the tiles' bytes, the scales
+        mbar_init(empty + 8 * lane, share);  // the consumers
+        fence_mbar_init();
+    }
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     long long N;
     int WS;
-    decode_prologue<T, D, C::WARPS, C::RING_BYTES / 8>(prm, reinterpret_cast<long long *>(smem_b8), starts, N, WS);
-    const int slice = static_cast<int>(blockIdx.x) * C::WARPS + warp;
-    if (slice >= WS) return;  // from here on every warp runs alone on its slice
-    const long long s_lo = N * slice / WS, s_hi = N * (slice + 1) / WS;
-    const int nb_w = static_cast<int>(s_hi - s_lo);
-
-    unsigned char *ring = smem_b8 + warp * C::WARP_RING;
-    const uint32_t ring_s = smem_addr(ring);
-    const uint32_t bars = smem_addr(smem_b8 + C::OFF_BAR) + warp * C::NSTAGE * 8;
-    const float *scale_slots = reinterpret_cast<const float *>(smem_b8 + C::OFF_SCALE) + warp * C::NSTAGE * 2;
-    const uint32_t scale_s = smem_addr(scale_slots);
-    if (lane == 0) {
-#pragma unroll
-        for (int s = 0; s < C::NSTAGE; ++s) mbar_init(bars + 8 * s, 3);  // lane 0's bytes, two scales
-        fence_mbar_init();
+    decode_prologue<T, D, C::RING_BYTES / 8, C::THREADS>(prm, reinterpret_cast<long long *>(smem_b8), starts,
+                                                         C::WARPS / share, N, WS);
+    __syncthreads();  // the barriers, and `starts` where the prologue had no sequences to scan
+    if (warp == C::WARPS) {
+        block8_produce<D>(b8, &tm_k, &tm_v, smem_b8, starts, N, WS);
+        return;
     }
-    __syncwarp();
-    Cursor cc{0, starts[5 * warp], starts[5 * warp + 1], starts[5 * warp + 3], starts[5 * warp + 4],
-              starts[5 * warp + 2]};
-
-    // ---- issue side, as in decode_kernel: block k at cursor ic into stage k % NSTAGE
-    int tb_u = -1, tbase = 0, tw = 0;
-    uint32_t bad_mask = 0;
-    auto issue = [&](int k, const Cursor &ic) {
-        const int u = ic.b * Hk + ic.hk;
-        if (u != tb_u || ic.blk >= tbase + 32) {
-            tb_u = u;
-            tbase = ic.blk;
-            const int e = tbase + lane;
-            tw = e < min(ic.nblk, prm.max_blocks_per_seq)
-                     ? __ldg(prm.block_tables + static_cast<size_t>(ic.b) * prm.max_blocks_per_seq + e)
-                     : 0;
-        }
-        int pb = __shfl_sync(0xffffffffu, tw, ic.blk - tbase);
-        const int s = k % C::NSTAGE;
-        if (pb < 0 || pb >= prm.num_blocks) {
-            if (lane == 0) flag_status(PA_STATUS_BAD_BLOCK_ID);
-            pb = 0;
-            bad_mask |= 1u << s;
-        } else {
-            bad_mask &= ~(1u << s);
-        }
-        const uint32_t bar = bars + 8 * s;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
-            const uint32_t dst = ring_s + s * C::STAGE_BYTES;
-            const uint64_t pol = policy_evict_normal();
-            tma_load_3d_policy(dst, &tm_k, 0, ic.hk, pb * kBlockSize, bar, pol);
-            tma_load_3d_policy(dst + kBlockSize * D, &tm_v, 0, ic.hk, pb * kBlockSize, bar, pol);
-        }
-        if (lane < 2) {
-            const float *src = (lane == 0 ? b8.k_scales : b8.v_scales) + static_cast<size_t>(pb) * Hk + ic.hk;
-            cp_async4(scale_s + 8 * s + 4 * lane, src);
-            cp_async_arrive(bar);
-        }
-    };
-    Cursor icur = cc;  // the last block fetched
-    for (int i = 0; i < min(C::NSTAGE, nb_w); ++i) {
-        if (i > 0) cursor_advance(icur, 1, prm);
-        issue(i, icur);
-    }
+    const int slice = static_cast<int>(blockIdx.x) * (C::WARPS / share) + group;
+    if (slice >= WS) return;
+    const int nb_w = static_cast<int>(N * (slice + 1) / WS - N * slice / WS);
+    const int stage_bytes = 2 * share * C::TILE;
+    const unsigned char *ring = smem_b8 + group * C::NSTAGE * stage_bytes + sub * C::TILE;  // this head's K of stage 0
+    const int4 *metas = reinterpret_cast<const int4 *>(smem_b8 + C::OFF_META) + group * C::NSTAGE;
+    const float2 *scale_slots = reinterpret_cast<const float2 *>(smem_b8 + C::OFF_SCALE) + warp * C::NSTAGE;
 
     // The unit's queries as the second operand of K Q^T: lane (gid, tid) holds head gid's
     // dims 16 tid + 4 s + {0..3} (s < 4), and 64 dims further on for s >= 4. factor[j]:
     // what a product of head 2 tid + j is multiplied by, short of the key scale.
     uint32_t qf[4 * KC][2];
     float factor[2];
-    auto load_q = [&](const Cursor &x) {
+    auto load_q = [&](int u) {
         float f[16 * KC];
         float amax = 0.f;
         if (gid < G) {
-            const T *row = static_cast<const T *>(prm.q) + (static_cast<size_t>(x.b) * prm.num_heads + x.hk * G + gid) * D;
+            const T *row = static_cast<const T *>(prm.q) + (static_cast<size_t>(u) * G + gid) * D;
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -228,33 +323,21 @@ __global__ void __launch_bounds__(Block8Cfg<D, G>::THREADS, 1)
         factor[1] = __shfl_sync(0xffffffffu, up, 8 * tid + 4);
     };
 
-    // Running state of heads 2 tid + j. O^T tile i: o[i][0], [1] are column 2 VW... of the
-    // lane's D / 8 output columns: column 2 i of heads 2 tid, 2 tid + 1, then column 2 i + 1.
+    // Running state of heads 2 tid + j. The lane's output columns are gid * D / 8 + c;
+    // o[i][j] is column 2 i, o[i][2 + j] column 2 i + 1 of head 2 tid + j.
     float o[TILES][4];
-    float l[2];   // this lane's share of the sums
-    float m[2];   // running max of the scores, or of an older one within 2^8
-    float r[2];   // the same of score + log2(v_scale), less kHeadroom: the unit of O
-    auto reset_state = [&]() {
-#pragma unroll
-        for (int i = 0; i < TILES; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            l[j] = 0.f;
-            m[j] = -CUDART_INF_F;
-            r[j] = -CUDART_INF_F;
-        }
-    };
-    const int t_lo = (kTau<D> >> (4 * gid)) & 7;               // token of this lane's score rows gid, gid + 8 (+ 8)
-    const int v_lo = (kTau<D> >> (8 * tid)) & 7;               // tokens of value rows 2 tid, 2 tid + 1 (and + 8)
+    float l[2];  // this lane's share of the sums
+    float m[2];  // running max of the scores, or of an older one within 2^8
+    float r[2];  // the same of score + log2(v_scale), less kHeadroom: the unit of O
+    const int t_lo = (kTau<D> >> (4 * gid)) & 7;  // token of this lane's score rows gid, gid + 8 (+ 8)
+    const int v_lo = (kTau<D> >> (8 * tid)) & 7;  // tokens of value rows 2 tid, 2 tid + 1 (and + 8)
     const int v_hi = (kTau<D> >> (8 * tid + 4)) & 7;
 
-    auto close_segment = [&]() {
-        const long long u_lo = s_lo + cc.r - cc.blk, u_hi = u_lo + cc.nblk;  // the unit's positions
-        const bool whole = u_lo >= s_lo && u_hi <= s_hi;
-        const int u = cc.b * Hk + cc.hk;
-        const size_t slot = static_cast<size_t>(slice) + u;
+    // A segment ends: the unit's output if the whole unit lies in this slice, else the
+    // segment's partial (m, l, O).
+    auto close_segment = [&](int lu, bool whole) {
+        const size_t u = static_cast<size_t>(lu) * share + sub;  // (sequence, KV head)
+        const size_t slot = (static_cast<size_t>(slice) + lu) * share + sub;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -263,51 +346,51 @@ __global__ void __launch_bounds__(Block8Cfg<D, G>::THREADS, 1)
             if (g < G) {
                 float sc = m[j] == -CUDART_INF_F ? 0.f : exp2f(r[j] - m[j]);
                 if (whole) sc = l[j] > 0.f ? sc / l[j] : 0.f;
-                constexpr int COLS = 2 * TILES;  // output columns of this lane: gid * COLS ...
+                const size_t head = (whole ? u : slot) * G + g;
 #pragma unroll
                 for (int i = 0; i < TILES; i += 2) {
                     const float4 x = make_float4(o[i][j] * sc, o[i][2 + j] * sc, o[i + 1][j] * sc, o[i + 1][2 + j] * sc);
-                    if (whole)
-                        store_out4(static_cast<T *>(prm.out) +
-                                       (static_cast<size_t>(cc.b) * prm.num_heads + cc.hk * G + g) * D + gid * COLS + 2 * i,
-                                   x);
-                    else
-                        st_v4_keep(prm.ws_o + (slot * G + g) * D + gid * COLS + 2 * i, x);
+                    const size_t at = head * D + gid * (2 * TILES) + 2 * i;
+                    if (whole) store_out4(static_cast<T *>(prm.out) + at, x);
+                    else st_v4_keep(prm.ws_o + at, x);
                 }
                 if (gid == 0) {
                     if (!whole) {
-                        prm.ws_m[slot * G + g] = m[j];
-                        prm.ws_l[slot * G + g] = l[j];
+                        prm.ws_m[head] = m[j];
+                        prm.ws_l[head] = l[j];
                     } else if constexpr (EMIT) {
-                        prm.lse[static_cast<size_t>(u) * G + g] = m[j] + log2f(l[j]);
+                        prm.lse[head] = m[j] + log2f(l[j]);
                     }
                 }
             }
         }
-        if (lane == 0 && u_lo >= s_lo) {
-            int *rec = prm.ws_unit + 2 * static_cast<size_t>(u);
-            rec[0] = slice;
-            rec[1] = whole ? 1 : slice_of(u_hi - 1, N, WS) - slice + 1;
-        }
     };
 
-    reset_state();
-    bool need_q = true;
+    int s = 0;
+    uint32_t phase = 0;
     int k = 0;
     for (; k < nb_w; ++k) {
-        const int s = k % C::NSTAGE;
-        if (need_q) {
-            load_q(cc);
-            need_q = false;
-        }
-        const bool landed = mbar_wait(bars + 8 * s, (k / C::NSTAGE) & 1);
+        const bool landed = mbar_wait(full + 8 * s, phase);
         if (!__all_sync(0xffffffffu, landed)) break;
-        const int last_valid = cc.c - (cc.nblk - 1) * kBlockSize;
-        const int n_valid = ((bad_mask >> s) & 1u) ? 0 : (cc.blk == cc.nblk - 1 ? last_valid : kBlockSize);
-        const unsigned char *kb = ring + s * C::STAGE_BYTES;
-        const unsigned char *vb = kb + kBlockSize * D;
+        const int4 meta = metas[s];
+        const int n_valid = meta.z & kMetaRows;
+        if (meta.z & kMetaFirst) {
+            load_q(meta.x * share + sub);
+#pragma unroll
+            for (int i = 0; i < TILES; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                l[j] = 0.f;
+                m[j] = -CUDART_INF_F;
+                r[j] = -CUDART_INF_F;
+            }
+        }
+        const unsigned char *kb = ring + s * stage_bytes;
+        const unsigned char *vb = kb + share * C::TILE;
         if (n_valid > 0) {
-            const float ks = scale_slots[2 * s], vs = scale_slots[2 * s + 1];
+            const float2 scales = scale_slots[s];
 
             // ---- scores
             float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -324,15 +407,45 @@ __global__ void __launch_bounds__(Block8Cfg<D, G>::THREADS, 1)
                     mma_f16(w % 2 ? c1 : c0, a0, a1, a2, a3, qf[4 * c + w][0], qf[4 * c + w][1]);
                 }
             }
+            // V's words are read now, so that they are there when the softmax is done
+            uint32_t w0[VW], w1[VW], w2[VW], w3[VW];  // rows 2 tid, 2 tid + 1, and + 8
+            auto load_v = [&](uint32_t(&w)[VW], int t) {
+                if constexpr (VW == 4) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(vb + tile_at<D>(t, gid));
+                    w[0] = a.x;
+                    w[1] = a.y;
+                    w[2] = a.z;
+                    w[3] = a.w;
+                } else {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(vb + tile_at<D>(t, gid / 2) + 8 * (gid % 2));
+                    w[0] = a.x;
+                    w[1] = a.y;
+                }
+            };
+            load_v(w0, v_lo);
+            load_v(w1, v_hi);
+            load_v(w2, v_lo + 8);
+            load_v(w3, v_hi + 8);
             float x[4];  // rows gid, gid + 8 of heads 2 tid, 2 tid + 1: x[2 * row half + j]
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (c0[e] + c1[e]) * (factor[e & 1] * ks);
+            const float f0 = factor[0] * scales.x, f1 = factor[1] * scales.x;
+            x[0] = (c0[0] + c1[0]) * f0;
+            x[1] = (c0[1] + c1[1]) * f1;
+            x[2] = (c0[2] + c1[2]) * f0;
+            x[3] = (c0[3] + c1[3]) * f1;
             if (n_valid < kBlockSize) {
                 if (t_lo >= n_valid) x[0] = x[1] = -CUDART_INF_F;
                 if (t_lo + 8 >= n_valid) x[2] = x[3] = -CUDART_INF_F;
+                // rows past the context may hold NaN codes, and 0 * NaN is NaN
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    if (v_lo >= n_valid) w0[i] = 0u;
+                    if (v_hi >= n_valid) w1[i] = 0u;
+                    if (v_lo + 8 >= n_valid) w2[i] = 0u;
+                    if (v_hi + 8 >= n_valid) w3[i] = 0u;
+                }
             }
             if constexpr (EMIT) {
-                float *rows = prm.scores + ((static_cast<size_t>(cc.b) * Hk + cc.hk) * prm.score_rows + cc.blk * kBlockSize) * G;
+                float *rows = prm.scores + (static_cast<size_t>(meta.x * share + sub) * prm.score_rows + meta.y * kBlockSize) * G;
                 if (2 * tid < G) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -346,17 +459,14 @@ __global__ void __launch_bounds__(Block8Cfg<D, G>::THREADS, 1)
             }
 
             // ---- online softmax: references move only when a score passes one by more than 2^8
-            const float lv = __log2f(vs);
-            bool grow = false;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float top = fmaxf(x[j], x[2 + j]);
-                grow |= top > m[j] + 8.f || top + lv > r[j] + (kHeadroom + 8.f);
-            }
+            const float lv = __log2f(scales.y);
+            const float top0 = fmaxf(x[0], x[2]), top1 = fmaxf(x[1], x[3]);
+            const bool grow = top0 > m[0] + 8.f || top1 > m[1] + 8.f || top0 + lv > r[0] + (kHeadroom + 8.f) ||
+                              top1 + lv > r[1] + (kHeadroom + 8.f);
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float top = fmaxf(x[j], x[2 + j]);
+                    float top = j ? top1 : top0;
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                     const float m_new = fmaxf(m[j], top), r_new = fmaxf(r[j], top + lv - kHeadroom);
@@ -373,38 +483,17 @@ __global__ void __launch_bounds__(Block8Cfg<D, G>::THREADS, 1)
             }
             float pv[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = e & 1;
-                const float mj = m[j] == -CUDART_INF_F ? 0.f : m[j], rj = r[j] == -CUDART_INF_F ? 0.f : r[j];
-                l[j] += ex2_approx(x[e] - mj);
-                pv[e] = ex2_approx(x[e] + lv - rj);
+            for (int j = 0; j < 2; ++j) {
+                const float mj = m[j] == -CUDART_INF_F ? 0.f : m[j];
+                const float rj = lv - (r[j] == -CUDART_INF_F ? 0.f : r[j]);
+                l[j] += ex2_approx(x[j] - mj) + ex2_approx(x[2 + j] - mj);
+                pv[j] = ex2_approx(x[j] + rj);
+                pv[2 + j] = ex2_approx(x[2 + j] + rj);
             }
             const uint32_t b0 = transpose8x8(pack_f16(pv[0], pv[1]));
             const uint32_t b1 = transpose8x8(pack_f16(pv[2], pv[3]));
 
             // ---- O^T += V^T P
-            uint32_t w0[VW], w1[VW], w2[VW], w3[VW];  // rows 2 tid, 2 tid + 1, and + 8
-            auto load_v = [&](uint32_t(&w)[VW], int t) {
-                if constexpr (VW == 4) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(vb + tile_at<D>(t, gid));
-                    w[0] = a.x;
-                    w[1] = a.y;
-                    w[2] = a.z;
-                    w[3] = a.w;
-                } else {
-                    const uint2 a = *reinterpret_cast<const uint2 *>(vb + tile_at<D>(t, gid / 2) + 8 * (gid % 2));
-                    w[0] = a.x;
-                    w[1] = a.y;
-                }
-                // rows past the context may hold NaN codes, and 0 * NaN is NaN
-                if (t >= n_valid)
-#pragma unroll
-                    for (int i = 0; i < VW; ++i) w[i] = 0u;
-            };
-            load_v(w0, v_lo);
-            load_v(w1, v_hi);
-            load_v(w2, v_lo + 8);
-            load_v(w3, v_hi + 8);
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
                 // a word's columns 4 w .. 4 w + 3 are rows gid, gid + 8 of tiles 2 w and 2 w + 1
@@ -418,23 +507,17 @@ __global__ void __launch_bounds__(Block8Cfg<D, G>::THREADS, 1)
             }
         }
         __syncwarp();
-        Cursor nx = cc;
-        const int passed = k + 1 < nb_w ? cursor_advance(nx, 1, prm) : 0;
-        if (k + C::NSTAGE < nb_w) {
-            cursor_advance(icur, 1, prm);
-            issue(k + C::NSTAGE, icur);
+        if (lane == 0) mbar_arrive(empty + 8 * s);
+        if (++s == C::NSTAGE) {
+            s = 0;
+            phase ^= 1;
         }
-        if (passed > 0 || k + 1 == nb_w) {
-            close_segment();
-            reset_state();
-            need_q = true;
-        }
-        cc = nx;
+        if (meta.z & kMetaLast) close_segment(meta.x, meta.z & kMetaWhole);
     }
     if (k < nb_w) {
         // a bounded wait gave up: let copies still in flight land before the CTA ends
         for (int kk = k; kk < min(k + C::NSTAGE, nb_w); ++kk)
-            mbar_wait(bars + 8 * (kk % C::NSTAGE), (kk / C::NSTAGE) & 1);
+            mbar_wait(full + 8 * (kk % C::NSTAGE), (kk / C::NSTAGE) & 1);
     }
 }
 

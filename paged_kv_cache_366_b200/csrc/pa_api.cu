@@ -189,14 +189,14 @@ void place_partials(pa::DecodeParams *prm, const DecodeGeometry &g, const pa_sha
 // The two launches of a decode: the partition pass and the merge.
 enum DecodeParts { kPartials = 1, kMerge = 2, kBoth = 3 };
 
-// The merge of cut units, with the caller's stream and launch attributes.
+// The merge of units cut by `slices` slices, with the caller's stream and launch attributes.
 template <typename Tq, int G, int D, bool EMIT>
-int launch_merge(const pa::DecodeParams &p, const DecodeGeometry &geo, int warps, cudaLaunchConfig_t cfg) {
+int launch_merge(const pa::DecodeParams &p, int64_t slices, cudaLaunchConfig_t cfg) {
     // Four warps per unit when units average 16 slices or more (long
     // contexts): their slices are merged four ways at once. One otherwise:
     // fewer, smaller CTAs launch and finish sooner.
     const int64_t units = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
-    const bool wide = static_cast<int64_t>(geo.ctas) * warps >= 16 * units;
+    const bool wide = slices * p.share >= 16 * units;
     cfg.gridDim = dim3(static_cast<unsigned>(units), (G * D + 127) / 128);
     cfg.blockDim = dim3(wide ? 128 : 32);
     cfg.dynamicSmemBytes = 0;
@@ -235,7 +235,7 @@ int launch_decode(const pa::DecodeParams &prm, const DecodeGeometry &geo, int pa
         const cudaError_t e = cudaLaunchKernelEx(&cfg, pa::decode_kernel<Tq, Tc, D, G, EMIT>, p, tm_k, tm_v);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    if (parts & kMerge) return launch_merge<Tq, G, D, EMIT>(p, geo, C::WARPS, cfg);
+    if (parts & kMerge) return launch_merge<Tq, G, D, EMIT>(p, p.warps_total, cfg);
     return PA_OK;
 }
 
@@ -350,7 +350,8 @@ int decode_call(void *out, const void *q, const void *k_cache, const void *v_cac
     prm.num_seqs = num_seqs;
     prm.max_blocks_per_seq = max_blocks_per_seq;
     prm.num_heads = shape->num_heads;
-    prm.num_kv_heads = shape->num_kv_heads;
+    prm.num_kv_heads = prm.list_heads = shape->num_kv_heads;
+    prm.share = 1;
     prm.max_context_len = max_context_len;
     prm.scale_log2 = scale * 1.4426950408889634f;
     prm.v_scale = 1.f;
