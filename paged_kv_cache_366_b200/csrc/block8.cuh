@@ -60,6 +60,19 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     }
 }
 
+// The same for values known to be finite and within the code's range.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4_in_range(float a, float b, float c, float d) {
+    if constexpr (FMT == kBlockE4M3) {
+        return encode4<FMT>(a, b, c, d);
+    } else {
+        // x + 1.5 * 2^23 is a number whose unit is 1: its low byte is x to the nearest, ties to even
+        const uint32_t lo = __byte_perm(__float_as_uint(a + 12582912.f), __float_as_uint(b + 12582912.f), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(c + 12582912.f), __float_as_uint(d + 12582912.f), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    }
+}
+
 // Four codes of one word to two f16 pairs, (codes 0, 1) and (codes 2, 3), exactly:
 // E4M3 by the hardware conversion; INT8 as the low byte of 1024 + (code + 128),
 // an f16 whose unit is 1, less 1152.
@@ -126,7 +139,7 @@ struct Block8WriteParams {
 };
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(128) block8_write_kernel(const Block8WriteParams prm) {
+__global__ void __launch_bounds__(128, 6) block8_write_kernel(const Block8WriteParams prm) {
     constexpr int EPL = D / 32;  // elements of a row per lane: 4 or 2
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x % 32, Hk = prm.num_kv_heads;
@@ -140,40 +153,41 @@ __global__ void __launch_bounds__(128) block8_write_kernel(const Block8WritePara
     uint8_t *codes = is_v ? prm.v_codes : prm.k_codes;
     float *scales = is_v ? prm.v_scales : prm.k_scales;
 
-    // lane i: the block of token t0 - 1 + i (negative: padding, or out of range)
-    auto block_of = [&](int64_t t) -> int64_t {
-        if (t < 0 || t >= prm.num_tokens) return -1;
-        const int64_t s = __ldg(prm.slot_mapping + t);
-        if (s >= prm.num_slots) {
+    // lane i: the slot of token t0 - 1 + i (negative: padding, or out of range). Runs that
+    // start among tokens t0 .. t0 + chunk - 1, chunk <= 16, end by t0 + 30: lane 31.
+    int64_t mine = -1;
+    {
+        const int64_t t = t0 - 1 + lane;
+        if (t >= 0 && t < prm.num_tokens) mine = __ldg(prm.slot_mapping + t);
+        if (mine >= prm.num_slots) {
             if (which == 0) flag_status(PA_STATUS_BAD_SLOT);
-            return -1;
+            mine = -1;
         }
-        return s < 0 ? -1 : s / kBlockSize;
-    };
-    const int64_t mine = block_of(t0 - 1 + lane);
-    const int64_t before = __shfl_up_sync(0xffffffffu, mine, 1);
-    uint32_t starts = __ballot_sync(0xffffffffu, lane >= 1 && lane <= prm.chunk && mine >= 0 && mine != before);
+    }
+    const int64_t my_block = mine < 0 ? -1 : mine / kBlockSize;
+    const int64_t before = __shfl_up_sync(0xffffffffu, my_block, 1);
+    uint32_t starts = __ballot_sync(0xffffffffu, lane >= 1 && lane <= prm.chunk && mine >= 0 && my_block != before);
     while (starts) {
         const int at = __ffs(starts) - 1;
         starts &= starts - 1;
         const int64_t t = t0 - 1 + at;
-        const int64_t blk = __shfl_sync(0xffffffffu, mine, at);
+        const int64_t blk = __shfl_sync(0xffffffffu, my_block, at);
         // the run: token t + i in lane i, at most 16
-        int row = kBlockSize;
-        if (lane < kBlockSize && t + lane < prm.num_tokens) {
-            const int64_t s = __ldg(prm.slot_mapping + t + lane);
-            if (s >= 0 && s / kBlockSize == blk) row = static_cast<int>(s % kBlockSize);
-        }
+        const int64_t slot = __shfl_sync(0xffffffffu, mine, min(at + lane, 31));
+        int row = lane < kBlockSize && slot >= 0 && slot / kBlockSize == blk ? static_cast<int>(slot % kBlockSize)
+                                                                             : kBlockSize;
         const uint32_t in = __ballot_sync(0xffffffffu, row < kBlockSize);
         const int n = __ffs(~in) - 1;  // in's low bits in a row
         if (lane >= n) row = kBlockSize;
         const int first = __reduce_min_sync(0xffffffffu, row);
 
+        const int64_t pitch = static_cast<int64_t>(Hk) * D;  // elements of a token, bytes of its codes
+        const __nv_bfloat16 *first_row = src + (t * Hk + hk) * D + lane * EPL;
         uint32_t raw[kBlockSize][EPL / 2];  // bf16 pairs
 #pragma unroll
         for (int i = 0; i < kBlockSize; ++i) {
             if (i < n) {
-                const uint32_t *p = reinterpret_cast<const uint32_t *>(src + ((t + i) * Hk + hk) * D) + lane * (EPL / 2);
+                const uint32_t *p = reinterpret_cast<const uint32_t *>(first_row + i * pitch);
                 if constexpr (EPL == 4) {
                     const uint2 r = *reinterpret_cast<const uint2 *>(p);
                     raw[i][0] = r.x;
@@ -185,51 +199,74 @@ __global__ void __launch_bounds__(128) block8_write_kernel(const Block8WritePara
         }
         float *scale_at = scales + blk * Hk + hk;
         const float held = first > 0 ? *scale_at : 0.f;
-        float amax = 0.f;
+        // The largest magnitude, by bf16 pairs: NaN if there is one, infinite if there is one;
+        // then (rarely) again over the finite ones, and with the careful conversion below.
+        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kBlockSize; ++i)
             if (i < n)
 #pragma unroll
-                for (int j = 0; j < EPL / 2; ++j) {
-                    amax = fmaxf(amax, finite_abs(__uint_as_float(raw[i][j] << 16)));
-                    amax = fmaxf(amax, finite_abs(__uint_as_float(raw[i][j] & 0xffff0000u)));
-                }
-        const float need = exp2_int(scale_exponent<FMT>(warp_max(amax)));
+                for (int j = 0; j < EPL / 2; ++j)
+                    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(raw[i][j]));
+        // bf16 magnitudes order as their bits, NaN above infinity
+        uint32_t bits = max(top & 0x7fffu, top >> 16 & 0x7fffu);
+        bits = __reduce_max_sync(0xffffffffu, bits);
+        float amax = __uint_as_float(bits << 16);
+        const bool odd = bits >= 0x7f80u;
+        if (odd) {
+            amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < kBlockSize; ++i)
+                if (i < n)
+#pragma unroll
+                    for (int j = 0; j < EPL / 2; ++j) {
+                        amax = fmaxf(amax, finite_abs(__uint_as_float(raw[i][j] << 16)));
+                        amax = fmaxf(amax, finite_abs(__uint_as_float(raw[i][j] & 0xffff0000u)));
+                    }
+            amax = warp_max(amax);
+        }
+        const float need = exp2_int(scale_exponent<FMT>(amax));
         const float scale = fmaxf(held, need);
         uint8_t *block = codes + (blk * kBlockSize * Hk + hk) * D + lane * EPL;  // this lane's columns of row 0
-        const int64_t row_bytes = static_cast<int64_t>(Hk) * D;
         if (first > 0 && scale > held) {
             const float ratio = held / scale;
             for (int r = 0; r < first; ++r) {
                 float f[4];
                 if constexpr (EPL == 4) {
-                    uint32_t *p = reinterpret_cast<uint32_t *>(block + r * row_bytes);
+                    uint32_t *p = reinterpret_cast<uint32_t *>(block + r * pitch);
                     widen4_f32<FMT>(*p, f);
                     *p = encode4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
                 } else {
-                    uint16_t *p = reinterpret_cast<uint16_t *>(block + r * row_bytes);
+                    uint16_t *p = reinterpret_cast<uint16_t *>(block + r * pitch);
                     widen4_f32<FMT>(*p, f);
                     *p = static_cast<uint16_t>(encode4<FMT>(f[0] * ratio, f[1] * ratio, 0.f, 0.f));
                 }
             }
         }
         const float inv = 1.f / scale;
+        auto put = [&](auto encode) {
 #pragma unroll
-        for (int i = 0; i < kBlockSize; ++i) {
-            const int r = __shfl_sync(0xffffffffu, row, i);
-            if (i < n) {
-                const float x0 = __uint_as_float(raw[i][0] << 16) * inv;
-                const float x1 = __uint_as_float(raw[i][0] & 0xffff0000u) * inv;
-                if constexpr (EPL == 4) {
-                    const float x2 = __uint_as_float(raw[i][EPL / 2 - 1] << 16) * inv;
-                    const float x3 = __uint_as_float(raw[i][EPL / 2 - 1] & 0xffff0000u) * inv;
-                    *reinterpret_cast<uint32_t *>(block + r * row_bytes) = encode4<FMT>(x0, x1, x2, x3);
-                } else {
-                    *reinterpret_cast<uint16_t *>(block + r * row_bytes) =
-                        static_cast<uint16_t>(encode4<FMT>(x0, x1, 0.f, 0.f));
+            for (int i = 0; i < kBlockSize; ++i) {
+                const int r = __shfl_sync(0xffffffffu, row, i);
+                if (i < n) {
+                    const float x0 = __uint_as_float(raw[i][0] << 16) * inv;
+                    const float x1 = __uint_as_float(raw[i][0] & 0xffff0000u) * inv;
+                    if constexpr (EPL == 4) {
+                        const float x2 = __uint_as_float(raw[i][EPL / 2 - 1] << 16) * inv;
+                        const float x3 = __uint_as_float(raw[i][EPL / 2 - 1] & 0xffff0000u) * inv;
+                        *reinterpret_cast<uint32_t *>(block + r * pitch) = encode(x0, x1, x2, x3);
+                    } else {
+                        *reinterpret_cast<uint16_t *>(block + r * pitch) =
+                            static_cast<uint16_t>(encode(x0, x1, 0.f, 0.f));
+                    }
                 }
             }
-        }
+        };
+        // in range: finite, and not past the largest scale
+        if (!odd && amax * inv <= (FMT == kBlockE4M3 ? 448.f : 127.f))
+            put([](float a, float b, float c, float d) { return encode4_in_range<FMT>(a, b, c, d); });
+        else
+            put([](float a, float b, float c, float d) { return encode4<FMT>(a, b, c, d); });
         if (lane == 0 && scale != held) *scale_at = scale;
     }
 }

@@ -33,16 +33,19 @@ int sms_or_default() {
 // ---- rotary positions -----------------------------------------------------------
 
 template <typename T, bool FP8>
-int launch_rope(const pa::RopeParams &p, int64_t num_tokens, int D, cudaStream_t st) {
+int launch_rope(pa::RopeParams p, int64_t num_tokens, int D, cudaStream_t st) {
+    p.num_tokens = num_tokens;
     const int heads = p.num_heads + p.num_kv_heads + (p.v ? p.num_kv_heads : 0);
-    const int items = heads * (D * static_cast<int>(sizeof(T)) / 32);
-    const int threads = std::min(pa::kRopeThreads, std::max(64, (items + 31) / 32 * 32));
-    // one item a thread while the tokens' CTAs do not fill the SMs; then a CTA a token
-    const int split = (items + threads - 1) / threads;
-    const int by = num_tokens * split <= sms_or_default() ? split : 1;
-    const dim3 grid(static_cast<unsigned>(num_tokens), by);
-    if (D == 128) pa::rope_kernel<T, FP8, 128><<<grid, threads, 0, st>>>(p);
-    else pa::rope_kernel<T, FP8, 64><<<grid, threads, 0, st>>>(p);
+    const int rows = pa::kRopeThreads / (D * static_cast<int>(sizeof(T)) / 32);  // rows a CTA takes at once
+    // four tokens a CTA once that fills the SMs four times; while single tokens leave SMs idle, their
+    // rows are spread over as many CTAs as hold one round of them each
+    const int64_t sms = sms_or_default();
+    const int tokens = num_tokens >= 16 * sms ? pa::kRopeTokens : 1;
+    const int split = (heads + rows - 1) / rows;
+    const int by = num_tokens * split <= sms ? split : 1;
+    const dim3 grid(static_cast<unsigned>((num_tokens + tokens - 1) / tokens), by);
+    if (D == 128) pa::rope_kernel<T, FP8, 128><<<grid, pa::kRopeThreads, 0, st>>>(p, tokens);
+    else pa::rope_kernel<T, FP8, 64><<<grid, pa::kRopeThreads, 0, st>>>(p, tokens);
     return check_launch();
 }
 

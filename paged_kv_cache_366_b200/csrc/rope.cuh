@@ -12,9 +12,10 @@
 // hundredths of a radian. The top 32 bits go through sincospif.
 //
 // Bound by memory: a token moves 2 H D (q) + 4 Hk D (k, v) elements and computes
-// rot_dim / 2 angles, shared by all heads. One CTA a token (more when few tokens
-// would leave SMs idle, each taking some of the heads): its threads issue their
-// loads, then compute the token's angles once in shared memory while they fly.
+// rot_dim / 2 angles, shared by all heads. A CTA takes four tokens (one when there are few,
+// with more CTAs to a token while they would leave SMs idle): its threads issue their
+// first loads, then compute the tokens' angles once into shared memory while those fly.
+
 #pragma once
 
 #include <cstring>
@@ -30,7 +31,7 @@ struct RopeParams {
     const int64_t *slot_mapping;     // null: k_out is [T][Hk][D]
     const int64_t *positions;
     int64_t q_stride, k_stride, v_stride;  // elements between tokens
-    int64_t num_slots;
+    int64_t num_slots, num_tokens;
     int num_heads, num_kv_heads;
     float k_inv, v_inv;              // 1 / scale of an FP8 cache
     pa_rope_plan plan;
@@ -58,86 +59,93 @@ __device__ __forceinline__ uint2 e4m3_vec(const float (&f)[8], float inv) {
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-constexpr int kRopeThreads = 384;  // 32 + 2 * 8 heads of 128 bf16: one unit each
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;  // tokens of a CTA at most
 
 // T: float or bf16. FP8: the caches hold E4M3 codes (T is bf16); the rotated k is
 // quantized from fp32, without a rounding to bf16 in between.
 // A unit is two 16-byte vectors of one head: for a rotated pair column u the
 // vectors that hold its x and its y (half layout) or two neighbours (interleaved,
-// and dims past rot_dim, which pass through).
+// and dims past rot_dim, which pass through). A thread keeps its column u and goes
+// through the rows (q's, k's and v's heads of each of the CTA's tokens), two at a time.
+// Grid: x groups of `tokens` tokens, y parts of their rows.
 template <typename T, bool FP8, int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams prm) {
-    constexpr int V = 16 / sizeof(T);    // elements of a vector
-    constexpr int UNITS = D / V / 2;     // units of a head
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams prm, int tokens) {
+    constexpr int V = 16 / sizeof(T);             // elements of a vector
+    constexpr int UNITS = D / V / 2;              // units of a head
+    constexpr int ROWS = kRopeThreads / UNITS;    // rows the CTA takes at once
     // (cos, sin) of pair u * V + i at i * UNITS + u: neighbouring threads read neighbouring entries
-    __shared__ float2 turn[D / 2];
+    __shared__ float2 turn[kRopeTokens][D / 2];
+    __shared__ int64_t slots[kRopeTokens];
     // a paged decode that follows is a programmatic dependent: it may launch now and waits for this grid
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t t = blockIdx.x;
-    const int H = prm.num_heads, Hk = prm.num_kv_heads;
-    const int rot = prm.plan.rot_dim, half = rot / 2;
-    const bool split = !prm.plan.interleaved;
-    int64_t slot = t;
-    if (prm.slot_mapping) {
-        slot = __ldg(prm.slot_mapping + t);
-        if (slot >= prm.num_slots) {
-            if (blockIdx.y == 0 && threadIdx.x == 0) flag_status(PA_STATUS_BAD_SLOT);
-            slot = -1;
-        }
-    }
-    // items: the units of q's heads, of k's and of v's
-    const int total = (H + Hk + (prm.v ? Hk : 0)) * UNITS;
-    const int step = blockDim.x * gridDim.y;
-    int item = blockIdx.y * blockDim.x + threadIdx.x;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+    const int count = static_cast<int>(min(static_cast<int64_t>(tokens), prm.num_tokens - t0));
+    const int H = prm.num_heads, Hk = prm.num_kv_heads, heads = H + Hk + (prm.v ? Hk : 0);
+    const int half = prm.plan.rot_dim / 2, u = threadIdx.x % UNITS;
+    const bool split = !prm.plan.interleaved, turns = u * V < half;
+    // first elements of the two vectors, in rows that are rotated and in v's
+    const int e0 = split && turns ? u * V : 2 * u * V, e1 = split && turns ? u * V + half : e0 + V;
 
-    auto place = [&](int it, const uint4 *&src, int &head, int &u, int &kind, int &e0, int &e1) {
-        head = it / UNITS;
-        u = it % UNITS;
-        kind = head < H ? 0 : head < H + Hk ? 1 : 2;
-        const T *base;
-        if (kind == 0) {
-            base = static_cast<const T *>(prm.q) + t * prm.q_stride + head * D;
-        } else if (kind == 1) {
-            head -= H;
-            base = static_cast<const T *>(prm.k) + t * prm.k_stride + head * D;
-        } else {
-            head -= H + Hk;
-            base = static_cast<const T *>(prm.v) + t * prm.v_stride + head * D;
-        }
-        const bool apart = kind != 2 && split && u * V < half;
-        e0 = apart ? u * V : 2 * u * V;  // first element of either vector
-        e1 = apart ? u * V + half : e0 + V;
-        src = reinterpret_cast<const uint4 *>(base);
+    struct Row {
+        int t, head;  // of the CTA's tokens; of q's, k's, v's heads in a line
+        uint4 a, b;
     };
-
-    const uint4 *src;
-    int head, u, kind, e0, e1;
-    uint4 r0, r1;
-    if (item < total) {
-        place(item, src, head, u, kind, e0, e1);
-        r0 = __ldcs(src + e0 / V);
-        r1 = __ldcs(src + e1 / V);
-    }
-    if (threadIdx.x < half) {
-        const uint64_t phase = static_cast<uint64_t>(__ldg(prm.positions + t)) * prm.plan.step[threadIdx.x];
+    const int step = ROWS * gridDim.y;
+    Row next{0, static_cast<int>(blockIdx.y) * ROWS + static_cast<int>(threadIdx.x) / UNITS, {}, {}};
+    auto settle = [&]() {
+        while (next.head >= heads) {
+            next.head -= heads;
+            ++next.t;
+        }
+    };
+    auto fetch = [&]() {  // the row at `next`, which moves on
+        Row r = next;
+        if (r.t < count) {
+            const int64_t t = t0 + r.t;
+            const T *p;
+            if (r.head < H) p = static_cast<const T *>(prm.q) + t * prm.q_stride + r.head * D;
+            else if (r.head < H + Hk) p = static_cast<const T *>(prm.k) + t * prm.k_stride + (r.head - H) * D;
+            else p = static_cast<const T *>(prm.v) + t * prm.v_stride + (r.head - H - Hk) * D;
+            const bool v = r.head >= H + Hk;
+            r.a = __ldcs(reinterpret_cast<const uint4 *>(p + (v ? 2 * u * V : e0)));
+            r.b = __ldcs(reinterpret_cast<const uint4 *>(p + (v ? 2 * u * V + V : e1)));
+        }
+        next.head += step;
+        settle();
+        return r;
+    };
+    settle();
+    Row r0 = fetch(), r1 = fetch();
+    for (int i = threadIdx.x; i < count * half; i += kRopeThreads) {
+        const int t = i / half, f = i - t * half;
+        const uint64_t phase = static_cast<uint64_t>(__ldg(prm.positions + t0 + t)) * prm.plan.step[f];
         // nearest 32-bit fraction of a turn, as a signed one in half turns
         const int32_t frac = static_cast<int32_t>((phase + 0x80000000ull) >> 32);
         float s, c;
         sincospif(static_cast<float>(frac) * 0x1p-31f, &s, &c);
-        turn[threadIdx.x % V * UNITS + threadIdx.x / V] = make_float2(c * prm.plan.mscale, s * prm.plan.mscale);
+        turn[t][f % V * UNITS + f / V] = make_float2(c * prm.plan.mscale, s * prm.plan.mscale);
+    }
+    if (threadIdx.x < count) {
+        int64_t slot = t0 + threadIdx.x;
+        if (prm.slot_mapping) {
+            slot = __ldg(prm.slot_mapping + slot);
+            if (slot >= prm.num_slots) {
+                if (blockIdx.y == 0) flag_status(PA_STATUS_BAD_SLOT);
+                slot = -1;
+            }
+        }
+        slots[threadIdx.x] = slot;
     }
     __syncthreads();
-    for (; item < total; item += step) {
-        if (item >= step) {  // past the thread's first item
-            place(item, src, head, u, kind, e0, e1);
-            r0 = __ldcs(src + e0 / V);
-            r1 = __ldcs(src + e1 / V);
-        }
+    auto finish = [&](const Row &r) {
+        if (r.t >= count) return;
+        const bool is_v = r.head >= H + Hk;
         float a[V], b[V];
-        widen_vec(r0, a);
-        widen_vec(r1, b);
-        if (kind != 2 && u * V < half) {
-            const float2 *cs = turn + u;
+        widen_vec(r.a, a);
+        widen_vec(r.b, b);
+        if (turns && !is_v) {
+            const float2 *cs = turn[r.t] + u;
             if (split) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -149,33 +157,43 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             } else {
 #pragma unroll
                 for (int i = 0; i < V; i += 2) {
-                    const float2 p = cs[i / 2 * UNITS], r = cs[(V + i) / 2 * UNITS];
-                    const float x = a[i], y = a[i + 1], z = b[i], w = b[i + 1];
+                    const float2 p = cs[i / 2 * UNITS], w = cs[(V + i) / 2 * UNITS];
+                    const float x = a[i], y = a[i + 1], z = b[i], v = b[i + 1];
                     a[i] = x * p.x - y * p.y;
                     a[i + 1] = y * p.x + x * p.y;
-                    b[i] = z * r.x - w * r.y;
-                    b[i + 1] = w * r.x + z * r.y;
+                    b[i] = z * w.x - v * w.y;
+                    b[i + 1] = v * w.x + z * w.y;
                 }
             }
         }
-        if (kind == 0) {
-            uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(prm.q_out) + (t * H + head) * D);
-            o[e0 / V] = narrow_vec(a);
-            o[e1 / V] = narrow_vec(b);
-        } else if (slot >= 0) {  // a negative slot is padding
-            void *pool = kind == 1 ? prm.k_out : prm.v_out;
-            const int64_t row = (slot * Hk + head) * D;
-            if constexpr (FP8) {
-                const float inv = kind == 1 ? prm.k_inv : prm.v_inv;
-                uint8_t *o = static_cast<uint8_t *>(pool) + row;
-                *reinterpret_cast<uint2 *>(o + e0) = e4m3_vec(a, inv);
-                *reinterpret_cast<uint2 *>(o + e1) = e4m3_vec(b, inv);
-            } else {
-                uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(pool) + row);
-                o[e0 / V] = narrow_vec(a);
-                o[e1 / V] = narrow_vec(b);
-            }
+        const int f0 = is_v ? 2 * u * V : e0, f1 = is_v ? 2 * u * V + V : e1;
+        if (r.head < H) {
+            T *o = static_cast<T *>(prm.q_out) + ((t0 + r.t) * H + r.head) * D;
+            *reinterpret_cast<uint4 *>(o + f0) = narrow_vec(a);
+            *reinterpret_cast<uint4 *>(o + f1) = narrow_vec(b);
+            return;
         }
+        const int64_t slot = slots[r.t];
+        if (slot < 0) return;  // padding
+        const int hk = r.head - H - (is_v ? Hk : 0);
+        const int64_t row = (slot * Hk + hk) * D;
+        if constexpr (FP8) {
+            const float inv = is_v ? prm.v_inv : prm.k_inv;
+            uint8_t *o = static_cast<uint8_t *>(is_v ? prm.v_out : prm.k_out) + row;
+            *reinterpret_cast<uint2 *>(o + f0) = e4m3_vec(a, inv);
+            *reinterpret_cast<uint2 *>(o + f1) = e4m3_vec(b, inv);
+        } else {
+            T *o = static_cast<T *>(is_v ? prm.v_out : prm.k_out) + row;
+            *reinterpret_cast<uint4 *>(o + f0) = narrow_vec(a);
+            *reinterpret_cast<uint4 *>(o + f1) = narrow_vec(b);
+        }
+    };
+    while (r0.t < count) {
+        const Row a = r0, b = r1;
+        r0 = fetch();
+        r1 = fetch();
+        finish(a);
+        finish(b);
     }
 }
 
