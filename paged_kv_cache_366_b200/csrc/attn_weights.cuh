@@ -3,10 +3,15 @@
 //
 // A probability is known only once its head's whole denominator is, so the decode
 // kernels (EMIT) leave every score, and each head's log2 denominator lse, and this pass
-// adds 2^(score - lse). That costs 4 H bytes written and read back for an entry whose
-// K and V are 2 Hk D elements (3 % of a bf16 cache's bytes at 32/8 heads of 128, mostly
+// adds 2^(score - lse). That costs 4 H bytes written and read back for an entry whose K
+// and V are 2 Hk D elements (3 % of a bf16 cache's bytes at 32/8 heads of 128, mostly
 // kept by L2), where a second pass over K would cost half of them again. Each weight is
 // one thread's: no atomics, the same sums every run.
+//
+// Sharing one launch with the merge, each counting CTA summing its unit's partial
+// denominators itself, was slower (decode batch 64.3 us against 58.3): that sum is a chain
+// of loads in every CTA. Here the scores, the weights and the denominators are loaded at
+// once.
 #pragma once
 
 #include "decode.cuh"
@@ -14,38 +19,54 @@
 namespace pa {
 
 constexpr int kCountThreads = 256;
-constexpr int kCountEntries = 4 * kCountThreads;  // entries of a CTA
+constexpr int kCountEntries = 4 * kCountThreads;  // entries of a CTA: four a thread, a CTA's width apart
 
-// Grid: (units * chunks). Four neighbouring entries a thread.
+// A programmatic dependent of the merge. Grid: units * chunks.
 template <int G>
 __global__ void __launch_bounds__(kCountThreads) count_weights_kernel(const DecodeParams prm, float *weights,
                                                                       int width, int chunks) {
     const int u = blockIdx.x / chunks, b = u / prm.num_kv_heads;
+    const int i0 = (blockIdx.x - u * chunks) * kCountEntries + threadIdx.x;
     const int n = clamp_context(__ldg(prm.context_lens + b), decode_cap(prm), false);
-    const int i0 = (blockIdx.x % chunks) * kCountEntries + 4 * threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (i0 >= n) return;
-    float lse[G];
+    constexpr int VEC = G < 4 ? G : 4;  // an entry's scores by 4, 8 or 16 bytes, lanes side by side
+    float s[4][G], w[4], lse[G];
+    const float *rows = prm.scores + static_cast<size_t>(u) * prm.score_rows * G;
+    float *at = weights + static_cast<size_t>(u) * width;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * kCountThreads;
+        if (i >= n) continue;
+#pragma unroll
+        for (int g = 0; g < G; g += VEC) {
+            const float *p = rows + static_cast<size_t>(i) * G + g;
+            if constexpr (VEC == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p));
+                s[e][g] = v.x;
+                s[e][g + 1] = v.y;
+                s[e][g + 2] = v.z;
+                s[e][g + 3] = v.w;
+            } else if constexpr (VEC == 2) {
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(p));
+                s[e][g] = v.x;
+                s[e][g + 1] = v.y;
+            } else {
+                s[e][g] = __ldcg(p);
+            }
+        }
+        w[e] = at[i];
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g) lse[g] = __ldcg(prm.lse + static_cast<size_t>(u) * G + g);
-    float s[4 * G];  // rows are padded to 16 entries: four are always there
-    const float4 *row = reinterpret_cast<const float4 *>(prm.scores + (static_cast<size_t>(u) * prm.score_rows + i0) * G);
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-        const float4 v = __ldcg(row + i);
-        s[4 * i] = v.x;
-        s[4 * i + 1] = v.y;
-        s[4 * i + 2] = v.z;
-        s[4 * i + 3] = v.w;
-    }
-    float *w = weights + static_cast<size_t>(u) * width + i0;
+    for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * kCountThreads;
+        if (i >= n) continue;
+        float p = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (i0 + i < n) {
-            float p = 0.f;
-#pragma unroll
-            for (int g = 0; g < G; ++g) p += ex2_approx(s[i * G + g] - lse[g]);
-            w[i] += p;
-        }
+        for (int g = 0; g < G; ++g) p += ex2_approx(s[e][g] - lse[g]);
+        at[i] = w[e] + p;
     }
 }
 

@@ -3,7 +3,6 @@
 // launch geometry and template dispatch; included by pa_api.cu after its own helpers.
 #pragma once
 
-#include "attn_weights.cuh"
 #include "block8.cuh"
 #include "decode_block8.cuh"
 #include "evict.cuh"
@@ -104,7 +103,7 @@ int launch_decode_block8(const pa::Block8Params &b8, const DecodeGeometry &geo, 
     cfg.dynamicSmemBytes = C::SMEM;
     e = cudaLaunchKernelEx(&cfg, kernel, p, tm_k, tm_v);
     if (e != cudaSuccess) return cuda_fail(e);
-    return launch_merge<__nv_bfloat16, G, D, EMIT>(p.d, p.d.warps_total, cfg);
+    return launch_merge<__nv_bfloat16, G, D, EMIT>(p.d, cfg);
 }
 
 template <int FMT, int D, bool EMIT>
@@ -162,17 +161,6 @@ CountSpace count_space(const DecodeGeometry &g, int32_t num_seqs, int32_t max_co
     c.lse_at = c.scores_at + c.score_rows * num_seqs * s->num_heads * 4;
     c.bytes = c.lse_at + round16(static_cast<int64_t>(num_seqs) * s->num_heads * 4);
     return c;
-}
-
-template <int G>
-int launch_count(const pa::DecodeParams &prm, float *weights, int width, cudaStream_t st) {
-    const int64_t units = static_cast<int64_t>(prm.num_seqs) * prm.num_kv_heads;
-    const int chunks = (prm.max_context_len + pa::kCountEntries - 1) / pa::kCountEntries;
-    if (chunks == 0) return PA_OK;
-    if (units * chunks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
-    pa::count_weights_kernel<G><<<static_cast<unsigned>(units * chunks), pa::kCountThreads, 0, st>>>(prm, weights,
-                                                                                                     width, chunks);
-    return check_launch();
 }
 
 // The checks and parameters that decode over a block8 pool and weight-counting decode share.
@@ -492,30 +480,25 @@ int pa_decode_weights(void *out, float *weights, int32_t weights_width, const vo
     if (workspace_bytes < c.bytes) return PA_ERR_WORKSPACE;
     p.d.scores = reinterpret_cast<float *>(static_cast<char *>(workspace) + c.scores_at);
     p.d.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + c.lse_at);
+    if (static_cast<int64_t>(num_seqs) * shape->num_kv_heads *
+            ((max_context_len + pa::kCountEntries - 1) / pa::kCountEntries) > 0x7fffffff)
+        return PA_ERR_UNSUPPORTED;
     p.d.score_rows = static_cast<int>(c.score_rows);
+    p.d.weights = weights;
+    p.d.weights_width = weights_width;
     p.k_scales = k_scales;
     p.v_scales = v_scales;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int G = shape->num_heads / shape->num_kv_heads;
-    if (is_block8(shape)) {
-        rc = dispatch_block8<true>(shape, p, g, st);
-    } else if (shape->kv_fp8) {
-        rc = shape->head_dim == 128 ? dispatch_g<__nv_bfloat16, pa::fp8e4m3, 128, true>(G, p.d, g, kBoth, st)
-                                    : dispatch_g<__nv_bfloat16, pa::fp8e4m3, 64, true>(G, p.d, g, kBoth, st);
-    } else if (shape->dtype == PA_DTYPE_BF16) {
-        rc = shape->head_dim == 128 ? dispatch_g<__nv_bfloat16, __nv_bfloat16, 128, true>(G, p.d, g, kBoth, st)
-                                    : dispatch_g<__nv_bfloat16, __nv_bfloat16, 64, true>(G, p.d, g, kBoth, st);
-    } else {
-        rc = shape->head_dim == 128 ? dispatch_g<float, float, 128, true>(G, p.d, g, kBoth, st)
-                                    : dispatch_g<float, float, 64, true>(G, p.d, g, kBoth, st);
-    }
-    if (rc != PA_OK) return rc;
-    switch (G) {
-        case 1: return launch_count<1>(p.d, weights, weights_width, st);
-        case 2: return launch_count<2>(p.d, weights, weights_width, st);
-        case 4: return launch_count<4>(p.d, weights, weights_width, st);
-        default: return launch_count<8>(p.d, weights, weights_width, st);
-    }
+    if (is_block8(shape)) return dispatch_block8<true>(shape, p, g, st);
+    if (shape->kv_fp8)
+        return shape->head_dim == 128 ? dispatch_g<__nv_bfloat16, pa::fp8e4m3, 128, true>(G, p.d, g, kBoth, st)
+                                      : dispatch_g<__nv_bfloat16, pa::fp8e4m3, 64, true>(G, p.d, g, kBoth, st);
+    if (shape->dtype == PA_DTYPE_BF16)
+        return shape->head_dim == 128 ? dispatch_g<__nv_bfloat16, __nv_bfloat16, 128, true>(G, p.d, g, kBoth, st)
+                                      : dispatch_g<__nv_bfloat16, __nv_bfloat16, 64, true>(G, p.d, g, kBoth, st);
+    return shape->head_dim == 128 ? dispatch_g<float, float, 128, true>(G, p.d, g, kBoth, st)
+                                  : dispatch_g<float, float, 64, true>(G, p.d, g, kBoth, st);
 }
 
 int pa_evict(void *k_cache, void *v_cache, float *k_scales, float *v_scales, const float *weights,

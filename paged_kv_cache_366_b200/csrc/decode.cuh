@@ -196,6 +196,8 @@ struct DecodeParams {
     float v_scale;     // 1, or the FP8 value scale
     float *scores;     // weight-counting decode: [B * Hk][score_rows][G] scores in the log2 domain
     float *lse;        // weight-counting decode: [B][H], log2 of each head's softmax denominator
+    float *weights;    // weight-counting decode: [B][Hk][weights_width]
+    int weights_width;
     int score_rows;    // entries of one unit in `scores`, a multiple of the block size
 };
 
@@ -795,25 +797,14 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
 // slices from the lengths before the wait; larger ones read the records.
 constexpr int kMergeScanSeqs = 256;
 
-// EMIT: also write the log2 denominators of the cut units' heads.
-template <typename T, int G, int D, int MG, bool EMIT = false>
-__global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParams prm) {
-    __shared__ float4 sh_o[MG][32];
-    __shared__ float sh_m[MG][32], sh_l[MG][32];
-    const int u = blockIdx.x;
-    const int b = u / prm.num_kv_heads, hk = u % prm.num_kv_heads;
-    const int lu = u / prm.share;  // the list's unit: share divides num_kv_heads
-    const int lane = threadIdx.x % 32, grp = threadIdx.x / 32;
-    const int idx = 4 * (blockIdx.y * 32 + lane);
-    const bool col = idx < G * D;  // the same for every warp: lanes past G * D only take part in the barrier
-    const int cap = decode_cap(prm);
-    const int c_b = clamp_context(__ldg(prm.context_lens + b), cap, false);
-    if (c_b == 0) return;  // zero rows, written by the decode kernel
-    int first, nseg;
+// The slices of unit (b, hk), whose sequence has c_b > 0 tokens: the first, and
+// how many. Waits for the decode kernel (griddepcontrol.wait). The whole warp
+// takes part.
+__device__ __forceinline__ void unit_slices(const DecodeParams &prm, int b, int hk, int c_b, int &first, int &nseg) {
+    const int lane = threadIdx.x % 32, cap = decode_cap(prm);
     if (prm.num_seqs <= kMergeScanSeqs) {
-        // The unit's slices from the lengths alone (inputs, not written by the
-        // decode kernel), before the wait: the same sums as the decode kernel's
-        // prologue. A unit in one slice needs no merge and leaves at once.
+        // From the lengths alone (inputs, not written by the decode kernel), before
+        // the wait: the same sums as the decode kernel's prologue.
         long long below = 0, total = 0;
         for (int i = lane; i < prm.num_seqs; i += 32) {
             const int c = clamp_context(__ldg(prm.context_lens + i), cap, false);
@@ -831,16 +822,38 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         const int ws = static_cast<int>(min(static_cast<long long>(prm.warps_total), total));
         first = slice_of(u_lo, total, ws);
         nseg = slice_of(u_lo + nblk - 1, total, ws) - first + 1;
-        if (nseg <= 1) return;  // a whole unit: written by the decode kernel
         asm volatile("griddepcontrol.wait;" ::: "memory");
     } else {
         asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int lu = (b * prm.num_kv_heads + hk) / prm.share;  // the list's unit: share divides num_kv_heads
         first = __ldcg(prm.ws_unit + 2 * lu);
         nseg = __ldcg(prm.ws_unit + 2 * lu + 1);
-        if (nseg <= 1) return;  // a whole unit: written by the decode kernel
     }
+}
+
+// EMIT: also write the log2 denominators of the cut units' heads.
+template <typename T, int G, int D, int MG, bool EMIT = false>
+__global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParams prm) {
+    __shared__ float4 sh_o[MG][32];
+    __shared__ float sh_m[MG][32], sh_l[MG][32];
+    const int u = blockIdx.x;
+    const int b = u / prm.num_kv_heads, hk = u % prm.num_kv_heads;
+    const int lane = threadIdx.x % 32, grp = threadIdx.x / 32;
+    const int idx = 4 * (blockIdx.y * 32 + lane);
+    const bool col = idx < G * D;  // the same for every warp: lanes past G * D only take part in the barrier
+    const int cap = decode_cap(prm);
+    const int c_b = clamp_context(__ldg(prm.context_lens + b), cap, false);
+    if (c_b == 0) {  // zero rows, written by the decode kernel
+        // Every CTA waits for the decode kernel, or a grid of early leavers could end
+        // before it does and let the stream go on.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
+    int first, nseg;
+    unit_slices(prm, b, hk, c_b, first, nseg);
+    if (nseg <= 1) return;  // a whole unit: written by the decode kernel
+    const int lu = u / prm.share;  // the list's unit: share divides num_kv_heads
     const int g = col ? idx / D : 0, d = col ? idx % D : 0;
-    const int s0 = first + lu;
     float M = -CUDART_INF_F, Lsum = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = grp; p0 < nseg; p0 += 8 * MG) {
@@ -850,7 +863,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         for (int i = 0; i < 8; ++i) {
             const int p = p0 + i * MG;
             const bool in = col && p < nseg;
-            const size_t s = static_cast<size_t>(s0 + p) * prm.share + (hk - hk / prm.share * prm.share);
+            const size_t s = static_cast<size_t>(first + lu + p) * prm.share + (hk - hk / prm.share * prm.share);
             mp[i] = in ? __ldcg(prm.ws_m + s * G + g) : -CUDART_INF_F;
             lp[i] = in ? __ldcg(prm.ws_l + s * G + g) : 0.f;
             op[i] = in ? __ldcg(reinterpret_cast<const float4 *>(prm.ws_o + (s * G + g) * D + d))

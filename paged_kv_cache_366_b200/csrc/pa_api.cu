@@ -10,6 +10,7 @@
 
 #include "pa_common.cuh"
 #include "decode.cuh"
+#include "attn_weights.cuh"
 #include "prefill_sm100.cuh"
 #include "block_copy.cuh"
 #include "reshape_and_cache.cuh"
@@ -189,20 +190,30 @@ void place_partials(pa::DecodeParams *prm, const DecodeGeometry &g, const pa_sha
 // The two launches of a decode: the partition pass and the merge.
 enum DecodeParts { kPartials = 1, kMerge = 2, kBoth = 3 };
 
-// The merge of units cut by `slices` slices, with the caller's stream and launch attributes.
+// The merge of cut units, with the caller's stream and launch attributes; EMIT: and
+// the counting of weights after it.
 template <typename Tq, int G, int D, bool EMIT>
-int launch_merge(const pa::DecodeParams &p, int64_t slices, cudaLaunchConfig_t cfg) {
+int launch_merge(const pa::DecodeParams &p, cudaLaunchConfig_t cfg) {
     // Four warps per unit when units average 16 slices or more (long
     // contexts): their slices are merged four ways at once. One otherwise:
     // fewer, smaller CTAs launch and finish sooner.
     const int64_t units = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
-    const bool wide = slices * p.share >= 16 * units;
+    const bool wide = static_cast<int64_t>(p.warps_total) * p.share >= 16 * units;
     cfg.gridDim = dim3(static_cast<unsigned>(units), (G * D + 127) / 128);
     cfg.blockDim = dim3(wide ? 128 : 32);
     cfg.dynamicSmemBytes = 0;
-    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 4, EMIT>, p)
-                               : cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 1, EMIT>, p);
-    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+    cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 4, EMIT>, p)
+                         : cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 1, EMIT>, p);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if constexpr (EMIT) {
+        const int chunks = (p.max_context_len + pa::kCountEntries - 1) / pa::kCountEntries;
+        if (chunks == 0) return PA_OK;
+        cfg.gridDim = dim3(static_cast<unsigned>(units * chunks));
+        cfg.blockDim = dim3(pa::kCountThreads);
+        e = cudaLaunchKernelEx(&cfg, pa::count_weights_kernel<G>, p, p.weights, p.weights_width, chunks);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return PA_OK;
 }
 
 template <typename Tq, typename Tc, int D, int G, bool EMIT>
@@ -235,7 +246,7 @@ int launch_decode(const pa::DecodeParams &prm, const DecodeGeometry &geo, int pa
         const cudaError_t e = cudaLaunchKernelEx(&cfg, pa::decode_kernel<Tq, Tc, D, G, EMIT>, p, tm_k, tm_v);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    if (parts & kMerge) return launch_merge<Tq, G, D, EMIT>(p, p.warps_total, cfg);
+    if (parts & kMerge) return launch_merge<Tq, G, D, EMIT>(p, cfg);
     return PA_OK;
 }
 
