@@ -172,6 +172,14 @@ __device__ __forceinline__ void st_v4_keep(float *p, float4 v) {
                  : "memory");
 }
 
+// N (1, 2 or 4) neighbouring scores, in one store (p is aligned to their size).
+template <int N>
+__device__ __forceinline__ void st_scores(float *p, const float *v) {
+    if constexpr (N == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else if constexpr (N == 2) *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+    else *p = v[0];
+}
+
 struct DecodeParams {
     void *out;
     const void *q;
@@ -674,8 +682,9 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
                     float *row = prm.scores +
                                  ((static_cast<size_t>(cc.b) * Hk + cc.hk) * prm.score_rows + cc.blk * kBlockSize +
                                   t_own) * G + hmask;
+                    constexpr int N = C::NFIN < 4 ? C::NFIN : 4;
 #pragma unroll
-                    for (int f = 0; f < C::NFIN; ++f) row[f] = sc[f];
+                    for (int f = 0; f < C::NFIN; f += N) st_scores<N>(row + f, sc + f);
                 }
             }
 

@@ -366,6 +366,8 @@ __global__ void __launch_bounds__(Block8Cfg<D>::THREADS, 1)
         }
     };
 
+    // the first unit's queries, while its first block is on the way
+    load_q((starts[5 * group] * prm.list_heads + starts[5 * group + 1]) * share + sub);
     int s = 0;
     uint32_t phase = 0;
     int k = 0;
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(Block8Cfg<D>::THREADS, 1)
         const int4 meta = metas[s];
         const int n_valid = meta.z & kMetaRows;
         if (meta.z & kMetaFirst) {
-            load_q(meta.x * share + sub);
+            if (k > 0) load_q(meta.x * share + sub);
 #pragma unroll
             for (int i = 0; i < TILES; ++i)
 #pragma unroll
@@ -451,8 +453,7 @@ __global__ void __launch_bounds__(Block8Cfg<D>::THREADS, 1)
                     for (int h = 0; h < 2; ++h) {
                         const int t = t_lo + 8 * h;
                         if (t < n_valid) {
-                            if constexpr (G == 1) rows[t] = x[2 * h];
-                            else *reinterpret_cast<float2 *>(rows + t * G + 2 * tid) = make_float2(x[2 * h], x[2 * h + 1]);
+                            st_scores<(G == 1 ? 1 : 2)>(rows + t * G + 2 * tid, x + 2 * h);
                         }
                     }
                 }

@@ -101,6 +101,7 @@ int resident_of() {
 struct DecodeFit {
     int resident;
     int warps;
+    int min_blocks = 4;  // of the largest possible list for each slice, at least
 };
 
 template <typename Tq, typename Tc, int D, int G>
@@ -156,7 +157,7 @@ int decode_geometry(int32_t num_seqs, int32_t max_context_len, int32_t requested
         slices = (n_max * PA_BLOCK_SIZE + requested - 1) / requested;
     } else {
         const int64_t sms = sm_count() > 0 ? sm_count() : 148;
-        slices = std::min<int64_t>(sms * fit.resident * fit.warps, (n_max + 3) / 4);
+        slices = std::min<int64_t>(sms * fit.resident * fit.warps, (n_max + fit.min_blocks - 1) / fit.min_blocks);
     }
     const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>((slices + fit.warps - 1) / fit.warps, 65535));
     g->ctas = static_cast<int>(ctas);
@@ -191,19 +192,27 @@ void place_partials(pa::DecodeParams *prm, const DecodeGeometry &g, const pa_sha
 enum DecodeParts { kPartials = 1, kMerge = 2, kBoth = 3 };
 
 // The merge of cut units, with the caller's stream and launch attributes; EMIT: and
-// the counting of weights after it.
-template <typename Tq, int G, int D, bool EMIT>
+// the counting of weights after it. DEEP: units cut into 64 slices or more are
+// merged by sixteen warps (the block8 decode cuts short lists down to a block).
+template <typename Tq, int G, int D, bool EMIT, bool DEEP = false>
 int launch_merge(const pa::DecodeParams &p, cudaLaunchConfig_t cfg) {
     // Four warps per unit when units average 16 slices or more (long
     // contexts): their slices are merged four ways at once. One otherwise:
     // fewer, smaller CTAs launch and finish sooner.
     const int64_t units = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
-    const bool wide = static_cast<int64_t>(p.warps_total) * p.share >= 16 * units;
+    const int64_t slices = static_cast<int64_t>(p.warps_total) * p.share;
+    const bool wide = slices >= 16 * units;
     cfg.gridDim = dim3(static_cast<unsigned>(units), (G * D + 127) / 128);
     cfg.blockDim = dim3(wide ? 128 : 32);
     cfg.dynamicSmemBytes = 0;
-    cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 4, EMIT>, p)
-                         : cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 1, EMIT>, p);
+    cudaError_t e;
+    if (DEEP && slices >= 64 * units) {
+        cfg.blockDim = dim3(512);
+        e = cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, DEEP ? 16 : 4, EMIT>, p);
+    } else {
+        e = wide ? cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 4, EMIT>, p)
+                 : cudaLaunchKernelEx(&cfg, pa::decode_merge_kernel<Tq, G, D, 1, EMIT>, p);
+    }
     if (e != cudaSuccess) return cuda_fail(e);
     if constexpr (EMIT) {
         const int chunks = (p.max_context_len + pa::kCountEntries - 1) / pa::kCountEntries;
