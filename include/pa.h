@@ -417,9 +417,12 @@ int64_t pa_decode_block8_workspace_bytes(int32_t num_seqs, int32_t max_context_l
 
 /*
  * pa_decode_block8: pa_decode over a block8 pool (bf16 q and out). Arguments as
- * pa_decode, with the scales ([NB][Hk] each, any finite values >= 0). Scores, softmax
- * sums and outputs accumulate in fp32; q enters the products as f16 after division by a
- * power of two for each head, probabilities as f16.
+ * pa_decode, with the scales ([NB][Hk] each, any finite values >= 0); like it, calls that
+ * overlap on the GPU must not share a workspace. Scores, softmax sums and outputs
+ * accumulate in fp32; q enters the products as f16 after division by a power of two for
+ * each head, probabilities as f16 with 2^-32 of the largest as their smallest step.
+ * max_context_len and 16 * max_blocks_per_seq up to 2^30 (PA_ERR_UNSUPPORTED beyond), here
+ * and in pa_decode_weights and pa_evict.
  */
 int pa_decode_block8(void *out, const void *q, const void *k_codes, const void *v_codes, const float *k_scales,
                      const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
@@ -438,7 +441,8 @@ int pa_decode_block8(void *out, const void *q, const void *k_codes, const void *
  *   k_scales, v_scales : block8 pools' scales; NULL otherwise
  *   workspace : >= pa_decode_weights_workspace_bytes(...) bytes: pa_decode's, then
  *               B * H * (max_context_len rounded up to 16) scores and B * H sums, fp32
- * Each weight is written by one thread, so results repeat bit for bit.
+ * Each weight is written by one thread, so results repeat bit for bit. Calls that overlap
+ * on the GPU must not share a workspace. Three launches.
  */
 int64_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t max_context_len, int32_t partition_tokens,
                                           const pa_shape *shape);

@@ -126,6 +126,9 @@ int dispatch_block8(const pa_shape *s, const pa::Block8Params &p, const DecodeGe
                               : dispatch_block8_g<pa::kBlockInt8, 64, EMIT>(g, p, geo, st);
 }
 
+// Lengths and table widths up to this keep the kernels' int arithmetic in range.
+constexpr int32_t kMaxContext = 1 << 30;
+
 // KV heads that share a stage of the block8 decode.
 int block8_share(const pa_shape *s) { return s->num_kv_heads % 4 == 0 ? 4 : s->num_kv_heads % 2 == 0 ? 2 : 1; }
 
@@ -135,6 +138,7 @@ int block8_share(const pa_shape *s) { return s->num_kv_heads % 4 == 0 ? 4 : s->n
 // sequences of 16 tokens 8.1 instead of 15.0 (graph replays, 32/8 heads of 128).
 int geometry_of(int32_t num_seqs, int32_t max_context_len, int32_t partition_tokens, const pa_shape *s,
                 DecodeGeometry *g) {
+    if (max_context_len > kMaxContext) return PA_ERR_UNSUPPORTED;
     if (!is_block8(s)) return decode_geometry(num_seqs, max_context_len, partition_tokens, s, g);
     const int share = block8_share(s);
     pa_shape list = *s;
@@ -172,6 +176,7 @@ int fill_decode(pa::DecodeParams *prm, DecodeGeometry *g, void *out, const void 
                 int32_t partition_tokens, void *workspace, const pa_shape *s) {
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARGUMENT;
     if (max_blocks_per_seq < 1 || !std::isfinite(scale)) return PA_ERR_INVALID_ARGUMENT;
+    if (max_blocks_per_seq > kMaxContext / PA_BLOCK_SIZE) return PA_ERR_UNSUPPORTED;
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned(block_tables, 4) ||
         !aligned(context_lens, 4))
         return PA_ERR_ALIGNMENT;
@@ -518,6 +523,9 @@ int pa_evict(void *k_cache, void *v_cache, float *k_scales, float *v_scales, con
         !new_context_lens || !kept)
         return PA_ERR_INVALID_ARGUMENT;
     if (max_blocks_per_seq < 1 || weights_width < max_context_len) return PA_ERR_INVALID_ARGUMENT;
+    if (max_context_len > kMaxContext || max_blocks_per_seq > kMaxContext / PA_BLOCK_SIZE ||
+        dst_blocks_per_seq > kMaxContext / PA_BLOCK_SIZE || keep > kMaxContext)
+        return PA_ERR_UNSUPPORTED;
     // every kept entry has a place in the new tables
     if (dst_blocks_per_seq < 1 ||
         static_cast<int64_t>(dst_blocks_per_seq) * PA_BLOCK_SIZE < std::min(keep, max_context_len))

@@ -160,6 +160,7 @@ REFUSED = [(dict(out=None), -1), (dict(q=None), -1), (dict(k=None), -1), (dict(v
            (dict(B=-1), -1), (dict(top=-1), -1), (dict(scale=math.nan), -1), (dict(scale=math.inf), -1),
            (dict(part=100), -1), (dict(part=-64), -1), (dict(ws=None), -4), (dict(n=16), -4), (dict(ws=P(0x10008)), -3),
            (dict(q=P(0x10008)), -3), (dict(ks=P(0x10002)), -3), (dict(lens=P(0x10002)), -3), (dict(B=0, q=None), 0),
+           (dict(top=(1 << 30) + 1), -2), (dict(mb=(1 << 26) + 1), -2), (dict(mb=(1 << 31) - 1), -2),
            (dict(shape=shape(kv_fp8=2, num_heads=24)), -2), (dict(shape=shape(kv_fp8=3, dtype=0)), -2)]
 
 
@@ -171,7 +172,7 @@ def test_decode_block8_refusals(kw, code):
 @pytest.mark.parametrize("kw,code", REFUSED + [(dict(w=None), -1), (dict(width=63), -1), (dict(w=P(0x10002)), -3)])
 def test_decode_weights_refusals(kw, code):
     kw = dict(kw)
-    w, width = kw.pop("w", J_), kw.pop("width", 64)
+    w, width = kw.pop("w", J_), kw.pop("width", max(64, kw.get("top", 0)))
     a = decode_args(**kw)
     assert lib().pa_decode_weights(a[0], w, width, *a[1:]) == code
 
@@ -217,7 +218,8 @@ def evict_args(**kw):
     (dict(sinks=(1 << 31) - 1, recent=(1 << 31) - 1), -1),
     (dict(shape=shape(kv_fp8=2)), -1), (dict(shape=shape(kv_fp8=3), ks=A), -1), (dict(k=P(0x10008)), -3),
     (dict(kept=P(0x10002)), -3), (dict(shape=shape(kv_fp8=1)), -1), (dict(shape=shape(kv_fp8=9)), -1),
-    (dict(B=0, k=None), 0), (dict(shape=shape(head_dim=80)), -2),
+    (dict(B=0, k=None), 0), (dict(shape=shape(head_dim=80)), -2), (dict(keep=(1 << 30) + 1), -2),
+    (dict(db=1 << 27), -2), (dict(mb=1 << 27), -2), (dict(top=(1 << 30) + 1, width=(1 << 31) - 1, keep=8, sinks=0), -2),
 ])
 def test_evict_refusals(kw, code):
     assert lib().pa_evict(*evict_args(**kw)) == code

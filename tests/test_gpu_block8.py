@@ -330,3 +330,83 @@ def test_decode_in_a_graph_and_on_another_stream(pa):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ref)
+
+
+def test_decode_many_sequences(pa):
+    # more than 256 sequences: the merge finds its slices in the records the decode kernel leaves
+    rng = np.random.default_rng(31)
+    lens = [int(n) for n in rng.integers(0, 90, 300)]
+    check_decode(pa, rng, lens, 8, 2, 64, "e4m3")
+    check_decode(pa, rng, lens[:270] + [3000], 4, 4, 128, "int8")
+
+
+def test_decode_more_sequences_than_one_scan_holds(pa):
+    # 30000 sequences of one token or none: an output row is its value row
+    rng = np.random.default_rng(32)
+    B, H, Hk, D = 30000, 4, 2, 64
+    kc, ks = make_pool(rng, 50, Hk, D, "int8")
+    vc, vs = make_pool(rng, 50, Hk, D, "int8")
+    t = rng.integers(0, 50, (B, 1)).astype(np.int32)
+    lens = rng.integers(0, 2, B).astype(np.int32)
+    q = bf16(rng.standard_normal((B, H, D)))
+    out = run_decode(pa, q, kc, vc, ks, vs, t, lens, 0.1)
+    assert pa.pa_get_status() == 0
+    ref = bf16(R.dequantized(vc, vs, "int8")[t[:, 0], 0] * lens[:, None, None]).repeat_interleave(H // Hk, 1)
+    # one code times a power of two: exact up to the division by the softmax sum, which is 1
+    assert torch.equal(out.cpu().float(), ref.float())
+
+
+def test_decode_on_two_streams_at_once(pa):
+    rng = np.random.default_rng(33)
+    cases = []
+    for code, lens in (("e4m3", [2000, 300, 5]), ("int8", [700] * 6)):
+        q, kc, vc, ks, vs, t = decode_case(rng, lens, 32, 8, 128, code)
+        ref = run_decode(pa, q, kc, vc, ks, vs, t, lens, 0.1)
+        d = [dev(a) for a in (kc, vc, ks, vs, t, np.asarray(lens, np.int32))]
+        n = pa.pa_decode_block8_workspace_bytes(len(lens), max(lens), 0, pa.shape_of_block8(d[0], 32))
+        cases.append((q.cuda(), d, max(lens), torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(ref), ref,
+                      torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, d, top, ws, out, _, stream in cases:
+            pa.pa_decode_block8(out, q, *d, top, 0.1, 0, ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, _, _, out, ref, _ in cases:
+        assert torch.equal(out, ref)
+
+
+def test_high_blocks_past_32_bits(pa):
+    # a pool of 4.9 GB of codes: rows whose byte offsets need more than 32 bits are written, read and evicted
+    NB, Hk, D, H, n = 300000, 8, 128, 32, 40
+    rng = np.random.default_rng(34)
+    k, v = (torch.zeros(NB, 16, Hk, D, dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(NB, Hk, device="cuda") for _ in range(2))
+    t = np.array([[NB - 1, NB - 7, 270000]], np.int32)
+    slots = np.array([int(t[0, p // 16]) * 16 + p % 16 for p in range(n)], np.int64)
+    x = [bf16(rng.standard_normal((n, Hk, D))) for _ in range(2)]
+    pa.pa_cache_block8(x[0].cuda(), x[1].cuda(), k, v, ks, vs, dev(slots))
+    td, ld = dev(t), torch.tensor([n], dtype=torch.int32, device="cuda")
+    q = bf16(rng.standard_normal((1, H, D)))
+    w = torch.zeros(1, Hk, 48, device="cuda")
+    out = torch.empty(1, H, D, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(pa.pa_decode_weights_workspace_bytes(1, 48, 0, pa.shape_of_block8(k, H)), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_weights(out, w, q.cuda(), k, v, td, ld, 48, 0.1, 0, ws, k_scales=ks, v_scales=vs)
+    small = [np.zeros((3, 16, Hk, D), np.int8) for _ in range(2)], [np.zeros((3, Hk), np.float32) for _ in range(2)]
+    local = [p for p in range(n)]
+    (kc, ksr), (vc, vsr) = (R.write(x[i].double().numpy(), small[0][i], small[1][i], local, "int8") for i in range(2))
+    att = R.attend(q.double().numpy(), R.dequantized(kc, ksr, "int8"), R.dequantized(vc, vsr, "int8"), np.arange(3)[None], [n], 0.1, vsr)
+    assert np.all(np.abs(out.double().cpu().numpy() - att[0][0]) <= bounds(att, 2.0 ** -8))
+    dst = torch.tensor([[NB - 20]], dtype=torch.int32, device="cuda")
+    kept, new_w = torch.empty(1, Hk, 16, dtype=torch.int32, device="cuda"), torch.empty(1, Hk, 16, device="cuda")
+    new_lens = torch.empty(1, dtype=torch.int32, device="cuda")
+    pa.pa_evict(k, v, w, td, ld, dst, new_w, new_lens, kept, 2, 4, 48, k_scales=ks, v_scales=vs)
+    assert pa.pa_get_status() == 0
+    wh = w.cpu().numpy()
+    for h in range(Hk):
+        idx = R.select(wh[0, h], n, 16, 2, 4)
+        assert np.array_equal(kept[0, h].cpu().numpy(), idx)
+        for pool, scales, codes, s in ((v, vs, vc, vsr), (k, ks, kc, ksr)):
+            rows = R.values(codes[idx // 16, idx % 16, h], "int8") * s[idx // 16, h].astype(np.float64)[:, None]
+            scale = R.least_scale(rows, "int8")
+            assert float(scales[NB - 20, h]) == scale
+            assert np.array_equal(pool[NB - 20, :, h].cpu().numpy(), R.encode(rows / scale, "int8"))

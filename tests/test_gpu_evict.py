@@ -193,9 +193,14 @@ def test_evict_ragged(pa, kind, Hk, D, keep, sinks, recent):
 
 @pytest.mark.parametrize("kind", ["bf16", "int8"])
 def test_evict_long(pa, kind):
-    # rows whose keys fit in shared memory, and one whose keys do not
+    # rows of a cluster of CTAs, short ones beside them
     check_evict(pa, np.random.default_rng(51), kind, [20000, 9, 5000], 2, 64, 4097, 4, 1000)
     check_evict(pa, np.random.default_rng(52), kind, [60000, 1000], 1, 64, 777, 0, 10)
+
+
+def test_evict_row_too_long_for_shared_memory(pa):
+    # 430000 keys over eight CTAs: more than they hold, so each pass reads the weights again
+    check_evict(pa, np.random.default_rng(59), "fp8", [430000, 70], 1, 64, 100001, 4, 5000)
 
 
 def test_evict_ties_and_odd_weights(pa):

@@ -188,3 +188,33 @@ def test_rotate_write_then_decode_in_a_graph(pa):
         torch.cuda.synchronize()
         assert torch.equal(out, out_g) and torch.equal(kc, kg) and torch.equal(vc, vg)
     assert pa.pa_get_status() == 0
+
+
+def test_rotate_many_tokens(pa):
+    # enough tokens for four to a CTA, the last CTA not full; every row against the one-token calls
+    T, H, Hk, D = 16 * 148 + 3, 8, 1, 64
+    q, k = (torch.randn(T, h, D, device="cuda", dtype=torch.bfloat16) for h in (H, Hk))
+    pos = torch.randint(0, 1 << 20, (T,), device="cuda")
+    plan = pa.pa_rope_init(32, interleaved=True)
+    q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+    pa.pa_rope(q_out, k_out, q, k, pos, plan)
+    a, b = torch.empty_like(q), torch.empty_like(k)
+    for lo in range(0, T, 500):
+        s = slice(lo, lo + 500)
+        pa.pa_rope(a[s], b[s], q[s], k[s], pos[s], plan)
+    assert torch.equal(a, q_out) and torch.equal(b, k_out)
+    _near(q_out.double().cpu().numpy(), q.double().cpu().numpy(), pos.cpu().numpy(), 32, True, R.frequencies(32), 1.0, 2.0 ** -8)
+
+
+def test_rotate_and_cache_past_32_bits(pa):
+    # a pool of 4.6 GB: slots whose byte offsets need more than 32 bits
+    NB, H, Hk, D, T = 140000, 8, 8, 128, 3
+    kc, vc = (torch.zeros(NB, 16, Hk, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, k, v = (torch.randn(T, H, D, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    slots = torch.tensor([NB * 16 - 1, 0, 2200000], device="cuda")
+    q_out = torch.empty_like(q)
+    pos = torch.tensor([5, (1 << 31) - 1, 0], device="cuda")
+    pa.pa_rope_and_cache(q_out, q, k, v, kc, vc, slots, pos, pa.pa_rope_init(D))
+    assert pa.pa_get_status() == 0
+    assert torch.equal(vc.flatten(0, 1)[slots], v) and int(vc.count_nonzero()) == int(v.count_nonzero())
+    _near(kc.flatten(0, 1)[slots].double().cpu().numpy(), k.double().cpu().numpy(), pos.cpu().numpy(), D, False, R.frequencies(D), 1.0, 2.0 ** -8)
