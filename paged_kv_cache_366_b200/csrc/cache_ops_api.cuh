@@ -84,12 +84,8 @@ int launch_decode_block8(const pa::Block8Params &b8, const DecodeGeometry &geo, 
     p.d.warps_total = geo.ctas * (C::WARPS / p.d.share);
     CUtensorMap tm_k{}, tm_v{};
     const uint64_t rows = static_cast<uint64_t>(p.d.num_blocks) * pa::kBlockSize;
-    const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    // A row of codes is 128 or 64 bytes, its neighbours other heads': L2 fetches no more than the
-    // row (with 256-byte fetches eight 32 K contexts took 118.6 us instead of 101.9).
-    const CUtensorMapL2promotion fetch = D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
-    if (!pa::encode_3d_by_column(&tm_k, p.d.k_cache, D, p.d.num_kv_heads, rows, D, pa::kBlockSize, p.d.share, sw, fetch) ||
-        !pa::encode_3d_by_column(&tm_v, p.d.v_cache, D, p.d.num_kv_heads, rows, D, pa::kBlockSize, p.d.share, sw, fetch))
+    if (!pa::encode_codes(&tm_k, p.d.k_cache, D, p.d.num_kv_heads, rows, p.d.share) ||
+        !pa::encode_codes(&tm_v, p.d.v_cache, D, p.d.num_kv_heads, rows, p.d.share))
         return PA_ERR_UNSUPPORTED;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -4,15 +4,19 @@
 //   K[p] = k_codes[block][p % 16] * k_scales[block][hk], V likewise,
 //   block = block_tables[b][p / 16].
 //
-// The work list, its slices, the partials and the merge are decode_kernel's, with up to
-// four neighbouring KV heads to a list entry, which as many warps take from one stage:
-// the heads' rows of a token are neighbours in memory, and 128-byte pieces of them at
-// far apart times stream at 5.1 TB/s where four together PLACEHOLDER. What differs
-// beside that is the block step, because the bytes are half of a bf16 cache's: at the
-// copy bandwidth an SM has about 180 cycles for a block of one KV head, and the
-// packed-FMA step of decode_kernel takes over 750 issue slots. So here a block is two
-// small matrix products on the warp's tensor instructions (m16n8k16, f16 operands,
-// fp32 sums), about 220 issue slots:
+// The work list, its slices, the partials and the merge are decode_kernel's, but a list
+// entry is up to four neighbouring KV heads of a block, which as many warps take from one
+// stage: the heads' rows of a token are neighbours in memory. One head at a time, 128-byte
+// rows a kilobyte apart streamed at 5.1 TB/s; four together stream at 6.3 (64 contexts of
+// 4096 tokens, 8 KV heads of 128: 112.5 and 96.0 us).
+//
+// Producer warps walk the slices and issue every load, a lane a slice; the consumer warps
+// only compute. Four of them: one lane's loads hold up its warp's others, and a single
+// producer took 95.5 us for eight 32 K contexts where four take 87.6, and 77.8 instead of
+// 52.5 us with one KV head (twelve slices to serve). At the copy bandwidth an SM has about 180 cycles for a block of one
+// KV head, half of a bf16 cache's, and the packed-FMA step of decode_kernel takes over 750
+// issue slots. So the block step is two small matrix products on the warp's tensor
+// instructions (m16n8k16, f16 operands, fp32 sums), about 250 issue slots in all:
 //  * S^T[16 tokens][8 heads] = K Q^T. K's codes widen exactly to f16 in registers; the
 //    group's heads fill the 8 columns (the rest are 0). tcgen05 wants 64 or more rows of
 //    a product at once and the operands in shared memory; widening through shared memory
@@ -26,7 +30,7 @@
 //
 // Numbers. Scores, maxima, sums and O are fp32. q enters as f16 after division by its
 // head's power of two (so a bf16 value is exact down to 2^-22 of the head's largest);
-// p enters P V as f16 (relative 2^-11, under bf16's 2^-9). The key scale multiplies the
+// p enters P V as f16 (relative 2^-11; bf16 would be 2^-8). The key scale multiplies the
 // block's scores. The value scale joins the exponent: P V uses
 // 2^(s + log2(v_scale) - r), with r a running reference of its own, so that f16 keeps
 // its digits whatever the spread of scales between blocks; r stays kHeadroom below the
@@ -48,7 +52,24 @@ struct Block8Params {
     const float *k_scales, *v_scales;  // [NB][Hk]
 };
 
-// A CTA is WARPS consumer warps and a producer warp. `share` consumer warps (4, 2 or 1:
+// Map over a pool of codes [rows][heads][D] with its two outer dims traded, coordinates (x,
+// row, head): a box of 16 rows of `share` heads lands as `share` tiles of 16 rows.
+// L2 fetches a row of D bytes and no more: its neighbours are other heads' (with 256-byte
+// fetches eight 32 K contexts took 118.6 us instead of 101.9 when a stage was one head's).
+inline bool encode_codes(CUtensorMap *m, const void *base, int D, uint64_t heads, uint64_t rows, uint32_t share) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t d = static_cast<cuuint64_t>(D), dims[3] = {d, rows, heads};
+    const cuuint64_t strides[2] = {heads * d, d};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), kBlockSize, share};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A CTA is WARPS consumer warps and PRODUCERS producer warps. `share` consumer warps (4, 2 or 1:
 // the most that divide the KV heads) form a group that streams one slice, a KV head each:
 // a stage is one block's K and V tiles of `share` neighbouring heads.
 template <int D>
@@ -56,10 +77,11 @@ struct Block8Cfg {
     static constexpr int TILE = kBlockSize * D;      // codes of one block of one KV head, K or V
     static constexpr int WARPS = 12;
     static constexpr int NSTAGE = D == 128 ? 4 : 8;  // 16 KB in flight per consumer warp
-    static constexpr int THREADS = 32 * (WARPS + 1);
+    static constexpr int PRODUCERS = 4;
+    static constexpr int THREADS = 32 * (WARPS + PRODUCERS);
     static constexpr int RING_BYTES = WARPS * NSTAGE * 2 * TILE;
     // per group (at most WARPS) and stage; the scales per warp and stage
-    static constexpr int OFF_META = RING_BYTES;                       // a StageMeta
+    static constexpr int OFF_META = RING_BYTES;                       // what it holds (an int4, below)
     static constexpr int OFF_SCALE = OFF_META + WARPS * NSTAGE * 16;  // k_scale, v_scale
     static constexpr int OFF_FULL = OFF_SCALE + WARPS * NSTAGE * 8;   // an mbarrier
     static constexpr int OFF_EMPTY = OFF_FULL + WARPS * NSTAGE * 8;
@@ -129,7 +151,7 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// The producer warp: lane g walks the slice of group g, a few blocks ahead of its
+// A producer warp: each lane walks the slice of one group, a few blocks ahead of its
 // consumers. For every block it writes what they need to know, and sends the heads' K
 // and V (two TMA boxes of `share` tiles) and scales (4-byte cp.async each) on the stage's
 // full barrier.
@@ -138,7 +160,8 @@ __device__ __forceinline__ void block8_produce(const Block8Params &b8, const CUt
                                                unsigned char *smem, const int *starts, long long N, int WS) {
     using C = Block8Cfg<D>;
     const DecodeParams &prm = b8.d;
-    const int g = threadIdx.x % 32, share = prm.share, groups = C::WARPS / share;
+    const int share = prm.share, groups = C::WARPS / share;
+    const int g = (threadIdx.x % 32) * C::PRODUCERS + threadIdx.x / 32 - C::WARPS;  // the group served
     const int slice = static_cast<int>(blockIdx.x) * groups + g;
     const bool mine = g < groups && slice < WS;
     const long long s_lo = mine ? N * slice / WS : 0, s_hi = mine ? N * (slice + 1) / WS : 0;
@@ -270,7 +293,7 @@ __global__ void __launch_bounds__(Block8Cfg<D>::THREADS, 1)
     decode_prologue<T, D, C::RING_BYTES / 8, C::THREADS>(prm, reinterpret_cast<long long *>(smem_b8), starts,
                                                          C::WARPS / share, N, WS);
     __syncthreads();  // the barriers, and `starts` where the prologue had no sequences to scan
-    if (warp == C::WARPS) {
+    if (warp >= C::WARPS) {
         block8_produce<D>(b8, &tm_k, &tm_v, smem_b8, starts, N, WS);
         return;
     }

@@ -298,6 +298,21 @@ __device__ __forceinline__ void widen16(const uint4 &v, uint32_t (&h)[8]) {
     widen4_f16<FMT>(v.w, h[6], h[7]);
 }
 
+// The same through fp32, for any ratio: code * s * inv. Rare, and out of line: its registers
+// would cost the copy a third of its warps.
+template <int FMT>
+__device__ __noinline__ uint4 rescale16_any(uint4 v, float s, float inv) {
+    uint32_t h[8], w[4];
+    widen16<FMT>(v, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i]));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i + 1]));
+        w[i] = encode4<FMT>(a.x * s * inv, a.y * s * inv, b.x * s * inv, b.y * s * inv);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The largest |code| of 16, NaN aside.
 __device__ __forceinline__ float largest16(const uint32_t (&h)[8]) {
     uint32_t top = 0;
@@ -351,19 +366,12 @@ __device__ __forceinline__ void copy_rows(unsigned char *pool, float *scales, in
         for (int st = 0; st < STEPS; ++st) {
             const float ratio = s[st] * inv;
             if (ratio == 1.f) continue;
-            uint32_t h[8];
-            widen16<FMT>(v[st], h);
             if (power_of_two(ratio) && ratio <= 0x1p15f && s[st] <= 0x1p120f) {
+                uint32_t h[8];
+                widen16<FMT>(v[st], h);
                 v[st] = rescale16<FMT>(h, fmaxf(ratio, 0x1p-24f));
             } else {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i]));
-                    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i + 1]));
-                    w[i] = encode4<FMT>(a.x * s[st] * inv, a.y * s[st] * inv, b.x * s[st] * inv, b.y * s[st] * inv);
-                }
-                v[st] = make_uint4(w[0], w[1], w[2], w[3]);
+                v[st] = rescale16_any<FMT>(v[st], s[st], inv);
             }
         }
     }

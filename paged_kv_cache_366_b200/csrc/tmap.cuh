@@ -29,10 +29,9 @@ inline EncodeTiledFn encode_tiled_fn() {
 
 // Map over a row-major 3-D tensor [n2][n1][n0] (n0 innermost) of `elem`-byte
 // elements, with row strides s1 = n0 * elem and s2 = n1 * n0 * elem bytes.
-// Box (b0, b1, b2); `promotion`: how much of a miss L2 fetches. Returns false if the driver rejects it.
+// Box (b0, b1, b2). Returns false if the driver rejects it.
 inline bool encode_3d(CUtensorMap *m, const void *base, uint64_t n0, uint64_t n1, uint64_t n2, int elem, uint32_t b0,
-                      uint32_t b1, uint32_t b2, CUtensorMapSwizzle swizzle,
-                      CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+                      uint32_t b1, uint32_t b2, CUtensorMapSwizzle swizzle) {
     EncodeTiledFn fn = encode_tiled_fn();
     if (!fn) return false;
     const CUtensorMapDataType dt = elem == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -43,22 +42,7 @@ inline bool encode_3d(CUtensorMap *m, const void *base, uint64_t n0, uint64_t n1
     const cuuint32_t box[3] = {b0, b1, b2};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-              promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The same tensor with its two outer dims traded: coordinates (x, row of n2, row of n1). A box
-// of b1 rows of n2 and b2 of n1 lands as b2 tiles of b1 rows each.
-inline bool encode_3d_by_column(CUtensorMap *m, const void *base, uint64_t n0, uint64_t n1, uint64_t n2, uint32_t b0,
-                                uint32_t b1, uint32_t b2, CUtensorMapSwizzle swizzle,
-                                CUtensorMapL2promotion promotion) {
-    EncodeTiledFn fn = encode_tiled_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {n0, n2, n1};
-    const cuuint64_t strides[2] = {n1 * n0, n0};
-    const cuuint32_t box[3] = {b0, b1, b2};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Tiled 3-D TMA load of one box at element coordinates (x, y, z) into shared
