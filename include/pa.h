@@ -423,6 +423,8 @@ int64_t pa_decode_block8_workspace_bytes(int32_t num_seqs, int32_t max_context_l
  * each head, probabilities as f16 with 2^-32 of the largest as their smallest step.
  * max_context_len and 16 * max_blocks_per_seq up to 2^30 (PA_ERR_UNSUPPORTED beyond), here
  * and in pa_decode_weights and pa_evict.
+ * Several query tokens of one sequence (a verify chunk) are several rows with the same
+ * block table and each its own length.
  */
 int pa_decode_block8(void *out, const void *q, const void *k_codes, const void *v_codes, const float *k_scales,
                      const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,

@@ -44,18 +44,19 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 // ---- which entries stay ---------------------------------------------------------
 //
-// A radix select over the 32-bit keys, 11 + 11 + 10 bits, finds the smallest kept key
+// A radix select over the 32-bit keys, 9 + 9 + 9 + 5 bits, finds the smallest kept key
 // and how many of its equals stay (it ends early once all keys that share the digits so
 // far stay); then warps count what they keep of their part of the row, a scan gives each
 // its place, and a second look writes. A (sequence, KV head) is the work of one CTA, or
 // of a cluster of up to 8 for long rows: each takes a contiguous share, adds the bins it
 // has keys in to the first CTA's through distributed shared memory, and that one tells
-// the others the digit. (Every CTA reading all the others' 2048 bins instead made the
-// select of 64 rows of up to 32 K weights 109 us; one CTA a row took 42.) Bound by
-// latency: up to three rounds of histogram, barrier and scan over a few thousand keys a
-// CTA, which stay in shared memory, so that HBM sees the weights once.
+// the others the digit. (Every CTA reading all the others' bins instead made the select
+// of 64 rows of up to 32 K weights 109 us; one CTA a row took 42.) Bound by latency: up
+// to four rounds of histogram, barrier and scan over a few thousand keys a CTA, which stay
+// in shared memory, so that HBM sees the weights once. 64 sequences of 128 to 2048 entries
+// with 8 KV heads: 14.2 us (three rounds of 2048 bins: 15.1); eight of 9 to 32 K: 28.4.
 constexpr int kSelectThreads = 512;
-constexpr int kSelectBins = 2048;
+constexpr int kSelectBins = kSelectThreads;  // a bin a thread
 constexpr int kSelectShare = 4096;          // keys of a CTA, while 8 CTAs are enough for that
 constexpr int kSelectKeys = 50 * 1024;      // keys a CTA's shared memory holds at most
 constexpr int kSelectMaxCluster = 8;        // the portable cluster size
@@ -131,10 +132,10 @@ __global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const E
     uint32_t prefix = 0, mask = 0;  // the smallest kept key's digits so far
     int need = prm.keep;            // keys to keep among those that share them
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const int bins = pass == 2 ? 1024 : 2048;
-        for (int i = tix; i < bins; i += THREADS) hist[i] = 0;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = pass == 3 ? 0 : 23 - 9 * pass;
+        const int bins = pass == 3 ? 32 : kSelectBins;
+        hist[tix] = 0;
         __syncthreads();
         if (pass == 0) {
             for (int i0 = lo + tix; i0 < hi; i0 += 4 * THREADS) {
@@ -159,39 +160,28 @@ __global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const E
             }
         }
         __syncthreads();
-        const int *h = hist;
+        int c = tix < bins ? hist[tix] : 0;
         if (ranks > 1) {
-            for (int i = tix; i < bins; i += THREADS)
-                if (hist[i]) atomicAdd(&sums[i], hist[i]);
+            if (c) atomicAdd(&sums[tix], c);
             cluster.sync();
-            h = total;
         }
         if (rank == 0) {
-            // each thread: bins / THREADS bins from the top; the digit is where the running
-            // count from the top first reaches `need`
-            constexpr int PER = kSelectBins / THREADS;
-            const int per = bins / THREADS;
-            int c[PER], sum = 0, all;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                c[i] = i < per ? h[bins - 1 - (tix * per + i)] : 0;
-                sum += c[i];
-            }
-            int above = scan_before<WARPS>(sum, warp_sums, all);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (above < need && above + c[i] >= need) {  // one thread: its digit to every CTA
-                    for (int r = 0; r < ranks; ++r) {
-                        int *f = ranks > 1 ? cluster.map_shared_rank(found, r) : found;
-                        f[0] = bins - 1 - (tix * per + i);
-                        f[1] = above;
-                        f[2] = c[i];
-                    }
+            // thread t: bin t from the top; the digit is where the running count from the top
+            // first reaches `need`
+            const int bin = bins - 1 - tix;
+            const int *h = ranks > 1 ? total : hist;
+            c = bin >= 0 ? h[bin] : 0;
+            int all;
+            const int above = scan_before<WARPS>(c, warp_sums, all);
+            if (above < need && above + c >= need) {  // one thread: its digit to every CTA
+                for (int r = 0; r < ranks; ++r) {
+                    int *f = ranks > 1 ? cluster.map_shared_rank(found, r) : found;
+                    f[0] = bin;
+                    f[1] = above;
+                    f[2] = c;
                 }
-                above += c[i];
             }
-            if (ranks > 1 && pass < 2)
-                for (int i = 0; i < per; ++i) total[bins - 1 - (tix * per + i)] = 0;
+            total[tix] = 0;  // for the next round (scan_before's barriers are behind every read)
         }
         if (ranks > 1) cluster.sync();
         else __syncthreads();
@@ -253,7 +243,9 @@ __global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const E
 // 2 * rows * 2 * D * E bytes. A lane holds its 16-byte pieces of all 16 rows in registers,
 // so that they are in flight together. (A persistent grid whose warps look up their next
 // piece while they copy took longer, 48 against 39 us for the batch: the registers of the
-// look-ahead cost more warps than it hides.)
+// look-ahead cost more warps than it hides.) Measured: a bf16 batch of 64 sequences cut to 512
+// entries, 249 MB, 37 us (6.7 TB/s); eight E4M3 contexts cut to 8191, 128-byte rows from
+// anywhere, 270 MB, 57 us (4.7 TB/s).
 //
 // FMT >= 0 (block8): a new block's rows come from blocks of different scales; the new
 // scale is the least power of two for its rows' largest magnitude, and the codes are

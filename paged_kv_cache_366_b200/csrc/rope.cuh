@@ -15,6 +15,9 @@
 // rot_dim / 2 angles, shared by all heads. A CTA takes four tokens (one when there are few,
 // with more CTAs to a token while they would leave SMs idle): its threads issue their
 // first loads, then compute the tokens' angles once into shared memory while those fly.
+// 8192 tokens of 32 + 2 * 8 heads of 128 in bf16: 35.4 us, 0.87 of the measured copy
+// bandwidth (a token a CTA of 384 threads, one unit a thread: 45.8 us, waiting for angles).
+// One token: 2.7 us.
 
 #pragma once
 

@@ -410,3 +410,18 @@ def test_high_blocks_past_32_bits(pa):
             scale = R.least_scale(rows, "int8")
             assert float(scales[NB - 20, h]) == scale
             assert np.array_equal(pool[NB - 20, :, h].cpu().numpy(), R.encode(rows / scale, "int8"))
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_several_query_tokens_as_rows(pa, code):
+    # a verify chunk of 4 tokens at the end of each sequence: rows with one table and growing lengths
+    rng = np.random.default_rng(35)
+    lens = [4, 21, 100, 333]
+    q, kc, vc, ks, vs, t = decode_case(rng, lens, 16, 4, 128, code)
+    rows = np.repeat(t, 4, axis=0)
+    row_lens = [n - 3 + j for n in lens for j in range(4)]
+    q = bf16(rng.standard_normal((16, 16, 128)))
+    out = run_decode(pa, q, kc, vc, ks, vs, rows, row_lens, 0.1)
+    assert pa.pa_get_status() == 0
+    att = R.attend(q.double().numpy(), R.dequantized(kc, ks, code), R.dequantized(vc, vs, code), rows, row_lens, 0.1, vs)
+    assert np.all(np.abs(out.double().cpu().numpy() - np.stack([a[0] for a in att])) <= bounds(att, 2.0 ** -8))
