@@ -304,8 +304,13 @@ def pa_prefill_chunk(out, q, k_cache, v_cache, block_tables, cu_q_lens, context_
 
 
 def pa_copy_blocks(k_cache, v_cache, block_pairs, stream=None) -> None:
-    """Copy whole blocks inside the pool: block_pairs int64 [n, 2] of (src, dst), on the device."""
+    """Copy whole blocks inside the pool: block_pairs int64 [n, 2] of (src, dst), on the device.
+
+    A block8 pool's codes are copied as bytes; its scales' rows (k_scales[dst] = k_scales[src]) are the caller's.
+    """
     _same_dtype(k_cache, v_cache)
+    if k_cache.dtype == torch.int8:
+        k_cache, v_cache = k_cache.view(torch.uint8), v_cache.view(torch.uint8)
     _int(block_pairs, torch.int64, "block_pairs")
     shape = shape_of(k_cache, k_cache.shape[2], 1.0, 1.0)
     _check("pa_copy_blocks", lib.pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(block_pairs),
@@ -344,18 +349,25 @@ def _shape(num_heads, num_kv_heads, head_dim, block_size, num_blocks, dtype, kv_
                    num_blocks=num_blocks, dtype=dtype, kv_fp8=kv_fp8, k_scale=k_scale, v_scale=v_scale)
 
 
-def _device_of(*tensors) -> int:
-    """The one device of the tensors, which is the current one; all but None are contiguous."""
+def _device_of(tensors) -> int:
+    """The one device of the tensors, which is the current one; all are contiguous (None entries are skipped)."""
     dev = tensors[0].get_device()
+    if dev < 0:
+        raise ValueError("tensor must be on a CUDA device")
     for t in tensors:
         if t is not None:
-            if t.get_device() != dev or dev < 0:
+            if t.get_device() != dev:
                 raise ValueError("all tensors must be on one CUDA device")
             if not t.is_contiguous():
                 raise ValueError("tensor must be contiguous")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError("tensors are on cuda:%d, which is not the current device" % dev)
     return dev
+
+
+def _current_device() -> int:
+    # a CUDA tensor exists, so the runtime is up: the plain query, without torch.cuda's initialisation check
+    return torch._C._cuda_getDevice()
 
 
 def _stream_on(stream, dev: int) -> int:
@@ -403,7 +415,7 @@ def pa_rope(q_out, k_out, q, k, positions, plan: PaRopePlan, stream=None) -> Non
     Hk = k.shape[1]
     if q_out.shape != q.shape or k.shape != (T, Hk, D) or k_out.shape != k.shape or positions.shape != (T,):
         raise ValueError("q, q_out [T, H, D]; k, k_out [T, Hk, D]; positions [T]")
-    dev = _device_of(q_out, k_out, positions)
+    dev = _device_of((q_out, k_out, positions))
     shape = _shape(H, Hk, D, BLOCK_SIZE, 1, _dtype_code(dt), 0)
     _check("pa_rope", lib.pa_rope(q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
                                   _row_stride(q, dev, H, D), _row_stride(k, dev, Hk, D), positions.data_ptr(), T,
@@ -425,7 +437,7 @@ def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
     if (q_out.shape != q.shape or k.shape != rows or v.shape != rows or positions.shape != (T,)
             or slot_mapping.shape != (T,)):
         raise ValueError("q, q_out [T, H, D]; k, v [T, Hk, D]; slot_mapping, positions [T]")
-    dev = _device_of(q_out, k_cache, v_cache, slot_mapping, positions)
+    dev = _device_of((q_out, k_cache, v_cache, slot_mapping, positions))
     _check("pa_rope_and_cache",
            lib.pa_rope_and_cache(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                  _row_stride(q, dev, H, D), _row_stride(k, dev, Hk, D), _row_stride(v, dev, Hk, D),
@@ -493,7 +505,7 @@ def pa_cache_block8(k, v, k_codes, v_codes, k_scales, v_scales, slot_mapping, st
     rows = (T, shape.num_kv_heads, shape.head_dim)
     if k.shape != rows or v.shape != rows or slot_mapping.shape != (T,):
         raise ValueError("k, v must be [T, Hk, D] matching the pool; slot_mapping [T]")
-    dev = _device_of(k, v, k_codes, v_codes, k_scales, v_scales, slot_mapping)
+    dev = _device_of((k, v, k_codes, v_codes, k_scales, v_scales, slot_mapping))
     _check("pa_cache_block8",
            lib.pa_cache_block8(k.data_ptr(), v.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
                                k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, shape,
@@ -524,7 +536,7 @@ def pa_decode_block8(out, q, k_codes, v_codes, k_scales, v_scales, block_tables,
     _check_decode(out, q, block_tables, context_lens)
     B, H, D = q.shape
     shape = _pool_shape(k_codes, v_codes, H, D, q.dtype, 0.0, 0.0, k_scales, v_scales)
-    dev = _device_of(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens, workspace)
+    dev = _device_of((out, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens, workspace))
     _check("pa_decode_block8",
            lib.pa_decode_block8(out.data_ptr(), q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
                                 k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
@@ -555,7 +567,7 @@ def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_l
     shape = _pool_shape(k_cache, v_cache, H, D, q.dtype, k_scale, v_scale, k_scales, v_scales)
     if weights.dim() != 3 or weights.shape[0] != B or weights.shape[1] != shape.num_kv_heads:
         raise ValueError("weights must be [B, Hk, W]")
-    dev = _device_of(out, weights, q, k_cache, v_cache, block_tables, context_lens, workspace, k_scales, v_scales)
+    dev = _device_of((out, weights, q, k_cache, v_cache, block_tables, context_lens, workspace, k_scales, v_scales))
     _check("pa_decode_weights",
            lib.pa_decode_weights(out.data_ptr(), weights.data_ptr(), weights.shape[2], q.data_ptr(),
                                  k_cache.data_ptr(), v_cache.data_ptr(), _optional(k_scales), _optional(v_scales),
@@ -589,8 +601,8 @@ def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, dst_block_ta
             or new_weights.shape != (B, Hk, dst_block_tables.shape[1] * BLOCK_SIZE)):
         raise ValueError("context_lens, new_context_lens [B]; block_tables, dst_block_tables [B, .]; weights, kept "
                          "[B, Hk, .]; new_weights [B, Hk, 16 * dst blocks]")
-    dev = _device_of(k_cache, v_cache, weights, block_tables, context_lens, dst_block_tables, new_weights,
-                     new_context_lens, kept, k_scales, v_scales)
+    dev = _device_of((k_cache, v_cache, weights, block_tables, context_lens, dst_block_tables, new_weights,
+                      new_context_lens, kept, k_scales, v_scales))
     _check("pa_evict",
            lib.pa_evict(k_cache.data_ptr(), v_cache.data_ptr(), _optional(k_scales), _optional(v_scales),
                         weights.data_ptr(), weights.shape[2], block_tables.data_ptr(), block_tables.shape[1],

@@ -225,6 +225,52 @@ def test_evict_refusals(kw, code):
     assert lib().pa_evict(*evict_args(**kw)) == code
 
 
+# ---- the Python binding's own checks
+
+
+def test_binding_refusals():
+    """Wrong devices, types and shapes are ValueErrors before the library is called (CPU tensors here)."""
+    import torch
+    from paged_kv_cache_366_b200 import pa
+    bf, i32, i64 = torch.bfloat16, torch.int32, torch.int64
+    q, kv = torch.zeros(2, 8, 64, dtype=bf), torch.zeros(2, 2, 64, dtype=bf)
+    pool, codes, scales = torch.zeros(4, 16, 2, 64, dtype=bf), torch.zeros(4, 16, 2, 64, dtype=torch.int8), torch.ones(4, 2)
+    n64, tables, lens, w = torch.zeros(2, dtype=i64), torch.zeros(2, 3, dtype=i32), torch.ones(2, dtype=i32), torch.zeros(2, 2, 48)
+    kept, plan = torch.zeros(2, 2, 8, dtype=i32), pa.pa_rope_init(64)
+    calls = {
+        "rope": (pa.pa_rope, [q, kv, q, kv, n64, plan]),
+        "rope_and_cache": (pa.pa_rope_and_cache, [q, q, kv, kv, pool, pool, n64, n64, plan]),
+        "write": (pa.pa_cache_block8, [kv, kv, codes, codes, scales, scales, n64]),
+        "decode": (pa.pa_decode_block8, [q, q, codes, codes, scales, scales, tables, lens, 48, 0.1]),
+        "weights": (pa.pa_decode_weights, [q, w, q, pool, pool, tables, lens, 48, 0.1]),
+        "evict": (pa.pa_evict, [pool, pool, w, tables, lens, tables, w, lens, kept, 0, 0, 48]),
+    }
+    for name, (fn, args) in calls.items():
+        with pytest.raises(ValueError, match="CUDA device"):
+            fn(*args)  # everything right but the device
+    wrong = {
+        "rope": {0: q[:, :4], 1: kv.float(), 3: kv[:1], 4: n64.int()},
+        "rope_and_cache": {1: q.float(), 2: kv[:, :1], 4: pool[..., :32], 5: pool[:2], 6: n64[:1], 7: n64.int()},
+        "write": {0: kv.float(), 1: kv[:1], 2: codes.float(), 3: codes[:2], 4: scales.double(), 5: scales[:2], 6: n64.int()},
+        "decode": {0: q[:1], 1: q.float(), 2: pool, 4: scales[:, :1], 6: tables.long(), 7: lens[:1]},
+        "weights": {0: q.float(), 1: w[:, :1], 2: q[..., :32], 3: pool.float(), 4: pool[:1], 5: tables[0], 6: lens.long()},
+        "evict": {1: pool[:2], 2: w.double(), 3: tables[:1], 5: tables.long(), 6: w[..., :40], 8: kept[:, :1]},
+    }
+    for name, changes in wrong.items():
+        fn, args = calls[name]
+        for i, bad in changes.items():
+            with pytest.raises(ValueError) as e:
+                fn(*(bad if j == i else a for j, a in enumerate(args)))
+            assert "CUDA device" not in str(e.value), (name, i)
+    with pytest.raises(ValueError, match="both"):
+        pa.pa_decode_weights(*calls["weights"][1], k_scales=scales)
+    with pytest.raises(ValueError):
+        pa.shape_of_block8(pool, 8)
+    a, b = pa.shape_of_block8(codes, 8), pa.shape_of_block8(codes, 8)
+    a.num_heads = 2
+    assert b.num_heads == 8  # each caller has its own
+
+
 # ---- the reference's own pieces
 
 

@@ -425,3 +425,22 @@ def test_several_query_tokens_as_rows(pa, code):
     assert pa.pa_get_status() == 0
     att = R.attend(q.double().numpy(), R.dequantized(kc, ks, code), R.dequantized(vc, vs, code), rows, row_lens, 0.1, vs)
     assert np.all(np.abs(out.double().cpu().numpy() - np.stack([a[0] for a in att])) <= bounds(att, 2.0 ** -8))
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_copied_blocks_decode_the_same(pa, code):
+    # copy-on-write of a block8 pool: codes by pa_copy_blocks, scales' rows by the caller
+    rng = np.random.default_rng(36)
+    lens = [50, 33]
+    q, kc, vc, ks, vs, t = decode_case(rng, lens, 8, 2, 64, code)
+    ref = run_decode(pa, q, kc, vc, ks, vs, t, lens, 0.1)
+    free = np.setdiff1d(np.arange(kc.shape[0]), t[t >= 0])[:3]
+    src = np.array([t[0, 0], t[0, 3], t[1, 2]])
+    k, v, s_k, s_v = (dev(a) for a in (kc, vc, ks, vs))
+    pa.pa_copy_blocks(k, v, dev(np.stack([src, free], 1).astype(np.int64)))
+    for s in (s_k, s_v):
+        s[dev(free)] = s[dev(src)]
+    t2 = t.copy()
+    t2[0, 0], t2[0, 3], t2[1, 2] = free
+    out = run_decode(pa, q, k.cpu().numpy(), v.cpu().numpy(), s_k.cpu().numpy(), s_v.cpu().numpy(), t2, lens, 0.1)
+    assert torch.equal(out, ref) and pa.pa_get_status() == 0
