@@ -441,8 +441,9 @@ int pa_decode_block8(void *out, const void *q, const void *k_codes, const void *
  *               past the context are left alone; the caller zeroes a row before its
  *               sequence's first step (pa_evict leaves the free entries zero).
  *   k_scales, v_scales : block8 pools' scales; NULL otherwise
- *   workspace : >= pa_decode_weights_workspace_bytes(...) bytes: pa_decode's, then
- *               B * H * (max_context_len rounded up to 16) scores and B * H sums, fp32
+ *   workspace : >= pa_decode_weights_workspace_bytes(...) bytes: partials as pa_decode's
+ *               (short lists are cut into more slices), then fp32, B * H *
+ *               (max_context_len rounded up to 16) scores and B * H sums
  * Each weight is written by one thread, so results repeat bit for bit. Calls that overlap
  * on the GPU must not share a workspace. Three launches.
  */

@@ -44,7 +44,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 // ---- which entries stay ---------------------------------------------------------
 //
-// A radix select over the 32-bit keys, 9 + 9 + 9 + 5 bits, finds the smallest kept key
+// A radix select over the 32-bit keys, a bin a thread, finds the smallest kept key
 // and how many of its equals stay (it ends early once all keys that share the digits so
 // far stay); then warps count what they keep of their part of the row, a scan gives each
 // its place, and a second look writes. A (sequence, KV head) is the work of one CTA, or
@@ -54,9 +54,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // of 64 rows of up to 32 K weights 109 us; one CTA a row took 42.) Bound by latency: up
 // to four rounds of histogram, barrier and scan over a few thousand keys a CTA, which stay
 // in shared memory, so that HBM sees the weights once. 64 sequences of 128 to 2048 entries
-// with 8 KV heads: 14.2 us (three rounds of 2048 bins: 15.1); eight of 9 to 32 K: 28.4.
-constexpr int kSelectThreads = 512;
-constexpr int kSelectBins = kSelectThreads;  // a bin a thread
+// with 8 KV heads: about 12 us (512 threads and three rounds of 2048 bins: 15.1); eight of
+// 9 to 32 K: 28.4.
 constexpr int kSelectShare = 4096;          // keys of a CTA, while 8 CTAs are enough for that
 constexpr int kSelectKeys = 50 * 1024;      // keys a CTA's shared memory holds at most
 constexpr int kSelectMaxCluster = 8;        // the portable cluster size
@@ -79,13 +78,16 @@ __device__ __forceinline__ int scan_before(int v, int *warp_sums, int &all) {
     return inc - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
 }
 
-// Four CTAs an SM: a CTA mostly waits (for loads, shared-memory atomics, barriers), and
-// the rows of a batch of 64 sequences with 8 KV heads then fit the GPU at once.
-__global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const EvictParams prm, int keys_held) {
+// THREADS: 512, digits of 9 + 9 + 9 + 5 bits, or 256, four of 8. 2048 threads an SM: a CTA mostly waits (for loads, shared-memory
+// atomics, barriers), and the rows of a batch of 64 sequences with 8 KV heads then fit the
+// GPU at once.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(const EvictParams prm, int keys_held) {
     extern __shared__ __align__(16) uint32_t select_keys[];
-    constexpr int THREADS = kSelectThreads, WARPS = THREADS / 32;
-    __shared__ int hist[kSelectBins];     // this CTA's keys
-    __shared__ int total[kSelectBins];    // rank 0 of a cluster: all CTAs' keys
+    constexpr int WARPS = THREADS / 32, BITS = THREADS == 512 ? 9 : 8;
+    static_assert(THREADS == 1 << BITS, "a bin a thread");
+    __shared__ int hist[THREADS];         // this CTA's keys
+    __shared__ int total[THREADS];        // rank 0 of a cluster: all CTAs' keys
     __shared__ int warp_sums[WARPS];
     __shared__ int found[3];              // the digit, the keys above it, the keys in it
     __shared__ int counts[2];             // this CTA's keys above the threshold, and equal to it
@@ -126,15 +128,15 @@ __global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const E
     int *sums = ranks > 1 ? cluster.map_shared_rank(total, 0) : total;
     if (ranks > 1) {
         if (rank == 0)
-            for (int i = tix; i < kSelectBins; i += THREADS) total[i] = 0;
+            total[tix] = 0;
         cluster.sync();
     }
     uint32_t prefix = 0, mask = 0;  // the smallest kept key's digits so far
     int need = prm.keep;            // keys to keep among those that share them
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
-        const int shift = pass == 3 ? 0 : 23 - 9 * pass;
-        const int bins = pass == 3 ? 32 : kSelectBins;
+        const int above_digit = 32 - BITS * pass, shift = max(0, above_digit - BITS);
+        const int bins = 1 << (above_digit - shift);
         hist[tix] = 0;
         __syncthreads();
         if (pass == 0) {

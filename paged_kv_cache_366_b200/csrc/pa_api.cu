@@ -193,8 +193,9 @@ enum DecodeParts { kPartials = 1, kMerge = 2, kBoth = 3 };
 
 // The merge of cut units, with the caller's stream and launch attributes; EMIT: and
 // the counting of weights after it. DEEP: units cut into 64 slices or more are
-// merged by sixteen warps (the block8 decode cuts short lists down to a block).
-template <typename Tq, int G, int D, bool EMIT, bool DEEP = false>
+// merged by sixteen warps (block8 and counting decodes cut short lists down to a
+// block).
+template <typename Tq, int G, int D, bool EMIT, bool DEEP = EMIT>
 int launch_merge(const pa::DecodeParams &p, cudaLaunchConfig_t cfg) {
     // Four warps per unit when units average 16 slices or more (long
     // contexts): their slices are merged four ways at once. One otherwise:

@@ -110,6 +110,8 @@ def test_counting_cut_units_and_several_steps(pa, kind):
 
 
 def test_counting_gives_decodes_output(pa):
+    # bit for bit over block8 pools; the plain pools' decode cuts short lists differently, so there each of the two
+    # is within its bound of the exact output
     rng = np.random.default_rng(43)
     lens = [400, 17, 1]
     nb, t = tables_of(rng, lens)
@@ -123,7 +125,12 @@ def test_counting_gives_decodes_output(pa):
             pa.pa_decode_block8(ref, q, pool.k, pool.v, pool.kw["k_scales"], pool.kw["v_scales"], *args)
         else:
             pa.pa_decode(ref, q, pool.k, pool.v, *args, **pool.one)
-        assert torch.equal(out, ref), kind
+        if pool.kw:
+            assert torch.equal(out, ref), kind
+        else:
+            att = R.attend(q.double().cpu().numpy(), pool.k64, pool.v64, t, lens, 0.1)
+            tol = bounds(att, torch.finfo(pool.dtype).eps / 2)
+            assert np.all(np.abs((out.double() - ref.double()).cpu().numpy()) <= 2 * tol), kind
 
 
 # ---- eviction
