@@ -54,8 +54,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // of 64 rows of up to 32 K weights 109 us; one CTA a row took 42.) Bound by latency: up
 // to four rounds of histogram, barrier and scan over a few thousand keys a CTA, which stay
 // in shared memory, so that HBM sees the weights once. 64 sequences of 128 to 2048 entries
-// with 8 KV heads: about 12 us (512 threads and three rounds of 2048 bins: 15.1); eight of
-// 9 to 32 K: 28.4.
+// with 8 KV heads: 14.1 us under ncu (512 threads and three rounds of 2048 bins: 15.1);
+// eight of 9 to 32 K: 28.4.
 constexpr int kSelectShare = 4096;          // keys of a CTA, while 8 CTAs are enough for that
 constexpr int kSelectKeys = 50 * 1024;      // keys a CTA's shared memory holds at most
 constexpr int kSelectMaxCluster = 8;        // the portable cluster size
