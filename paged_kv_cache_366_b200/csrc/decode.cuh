@@ -256,7 +256,7 @@ __device__ __forceinline__ int slice_of(long long f, long long N, int W) {
 // `own` slices (at most THREADS): the list's block count N, its number of slices
 // WS, and for each slice of the CTA its first block in `starts` (5 ints: b, hk,
 // blk, c, nblk). Rows of sequences of length 0 are written as zeros here. `cum`
-// is CHUNK entries of shared memory, free again on return.
+// is CHUNK entries of shared memory, free again on return, for TMA writes too.
 template <typename Tq, int D, int CHUNK, int THREADS>
 __device__ __forceinline__ void decode_prologue(const DecodeParams &prm, long long *cum, int *starts, int own,
                                                 long long &N, int &WS) {
@@ -357,6 +357,9 @@ __device__ __forceinline__ void decode_prologue(const DecodeParams &prm, long lo
                 }
             }
             base = cum[n - 1];
+            // `cum` lies where the first blocks land. A barrier alone does not order these plain
+            // accesses before the TMA writes of another thread, which go by the async proxy.
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncthreads();
         }
     }
