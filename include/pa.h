@@ -440,6 +440,8 @@ int pa_decode_block8(void *out, const void *q, const void *k_codes, const void *
  *   weights   : fp32 [B][Hk][weights_width], weights_width >= max_context_len. Entries
  *               past the context are left alone; the caller zeroes a row before its
  *               sequence's first step (pa_evict leaves the free entries zero).
+ *               Entries of a block outside the pool (PA_STATUS_BAD_BLOCK_ID) take no
+ *               part: their weights stay, the others' are as without them.
  *   k_scales, v_scales : block8 pools' scales; NULL otherwise
  *   workspace : >= pa_decode_weights_workspace_bytes(...) bytes: partials as pa_decode's
  *               (short lists are cut into more slices), then fp32, B * H *

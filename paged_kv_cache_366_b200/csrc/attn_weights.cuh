@@ -3,10 +3,11 @@
 //
 // A probability is known only once its head's whole denominator is, so the decode
 // kernels (EMIT) leave every score, and each head's log2 denominator lse, and this pass
-// adds 2^(score - lse). That costs 4 H bytes written and read back for an entry whose K
-// and V are 2 Hk D elements (3 % of a bf16 cache's bytes at 32/8 heads of 128, mostly
-// kept by L2), where a second pass over K would cost half of them again. Each weight is
-// one thread's: no atomics, the same sums every run.
+// adds 2^(score - lse) (a bad block's entries have score -inf and add 0). That costs 4 H
+// bytes written and read back for an entry whose K and V are 2 Hk D elements (3 % of a
+// bf16 cache's bytes at 32/8 heads of 128, mostly kept by L2), where a second pass over K
+// would cost half of them again. Each weight is one thread's: no atomics, the same sums
+// every run.
 //
 // Sharing one launch with the merge, each counting CTA summing its unit's partial
 // denominators itself, was slower (decode batch 64.3 us against 58.3): that sum is a chain
@@ -60,7 +61,10 @@ __global__ void __launch_bounds__(kCountThreads) count_weights_kernel(const Deco
         w[e] = at[i];
     }
 #pragma unroll
-    for (int g = 0; g < G; ++g) lse[g] = __ldcg(prm.lse + static_cast<size_t>(u) * G + g);
+    for (int g = 0; g < G; ++g) {
+        lse[g] = __ldcg(prm.lse + static_cast<size_t>(u) * G + g);
+        if (lse[g] == -CUDART_INF_F) lse[g] = 0.f;  // every score is -inf (all blocks bad, say): 0 for each
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int i = i0 + e * kCountThreads;

@@ -772,6 +772,15 @@ __global__ void __launch_bounds__(DecodeCfg<Tc, D, G>::THREADS, 1)
                 }
             }
         }
+        if constexpr (EMIT) {
+            // A block outside the pool takes no part; its scores say so, as the workspace holds whatever was there.
+            if (n_valid == 0) {
+                const int n = (cc.blk == cc.nblk - 1 ? last_valid : kBlockSize) * G;
+                float *row = prm.scores +
+                             ((static_cast<size_t>(cc.b) * Hk + cc.hk) * prm.score_rows + cc.blk * kBlockSize) * G;
+                for (int i = lane; i < n; i += 32) row[i] = -CUDART_INF_F;
+            }
+        }
         __syncwarp();
         Cursor nx = cc;  // this warp's next block
         const int passed = k + 1 < nb_w ? cursor_advance(nx, 1, prm) : 0;

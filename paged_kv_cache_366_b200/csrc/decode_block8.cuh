@@ -98,7 +98,7 @@ struct Block8Cfg {
 };
 
 // What a stage holds, as one int4: the list's unit, its block, valid rows (0: a bad
-// table entry) with flags.
+// table entry) with flags, rows within the context.
 constexpr int kMetaFirst = 0x100, kMetaLast = 0x200, kMetaWhole = 0x400, kMetaRows = 0xff;
 
 // d += a b, a [16][16] (row-major fragments), b [16][8], f16 in, fp32 out.
@@ -219,7 +219,8 @@ __device__ __forceinline__ void block8_produce(const Block8Params &b8, const CUt
         if (go) {
             const int i = cc.blk - qbase;
             int pb = i == 0 ? cur[0] : i == 1 ? cur[1] : i == 2 ? cur[2] : cur[3];
-            int rows = cc.blk == cc.nblk - 1 ? cc.c - cc.blk * kBlockSize : kBlockSize;
+            const int in_context = cc.blk == cc.nblk - 1 ? cc.c - cc.blk * kBlockSize : kBlockSize;
+            int rows = in_context;
             if (pb < 0 || pb >= prm.num_blocks) {
                 flag_status(PA_STATUS_BAD_BLOCK_ID);
                 pb = 0;
@@ -232,7 +233,7 @@ __device__ __forceinline__ void block8_produce(const Block8Params &b8, const CUt
             meta[s] = make_int4(u, cc.blk,
                                 rows | (cc.blk == 0 || k == 0 ? kMetaFirst : 0) | (last ? kMetaLast : 0) |
                                     (whole ? kMetaWhole : 0),
-                                0);
+                                in_context);
             const uint32_t bar = full + 8 * s, dst = ring + s * 2 * tiles;
             const int head = cc.hk * share;
             mbar_arrive_expect_tx(bar, 2 * tiles);
@@ -535,6 +536,10 @@ __global__ void __launch_bounds__(Block8Cfg<D>::THREADS, 1)
                     mma_f16(o[2 * w + h], a0, a1, a2, a3, b0, b1);
                 }
             }
+        } else if constexpr (EMIT) {
+            // A block outside the pool takes no part; its scores say so, as the workspace holds whatever was there.
+            float *rows = prm.scores + (static_cast<size_t>(meta.x * share + sub) * prm.score_rows + meta.y * kBlockSize) * G;
+            for (int i = lane; i < meta.w * G; i += 32) rows[i] = -CUDART_INF_F;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + 8 * s);
