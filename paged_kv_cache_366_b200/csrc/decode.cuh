@@ -893,8 +893,9 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         float mc = M;
 #pragma unroll
         for (int i = 0; i < 8; ++i) mc = fmaxf(mc, mp[i]);
-        if (mc == -CUDART_INF_F) continue;
-        const float a = exp2f(M - mc);  // 0 while M is still -inf
+        // -inf: no score so far but -inf or NaN. O and l are then 0 (blocks skipped, scores of -inf)
+        // or NaN, and NaN must stay: a plain sum does both.
+        const float a = M == mc ? 1.f : exp2f(M - mc);
         O.x *= a;
         O.y *= a;
         O.z *= a;
@@ -902,8 +903,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         Lsum *= a;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (mp[i] == -CUDART_INF_F) continue;  // a slice whose blocks were all skipped
-            const float wt = exp2f(mp[i] - mc);
+            const float wt = mp[i] == mc ? 1.f : exp2f(mp[i] - mc);
             O.x += wt * op[i].x;
             O.y += wt * op[i].y;
             O.z += wt * op[i].z;
@@ -928,8 +928,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
 #pragma unroll
         for (int w = 0; w < MG; ++w) {
             const float mw = sh_m[w][lane];
-            if (mw == -CUDART_INF_F) continue;  // a warp with no slices, or only skipped ones
-            const float wt = exp2f(mw - Mt);
+            const float wt = mw == Mt ? 1.f : exp2f(mw - Mt);  // as above where both are -inf
             const float4 ow = sh_o[w][lane];
             Ot.x += wt * ow.x;
             Ot.y += wt * ow.y;

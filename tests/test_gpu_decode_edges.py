@@ -111,3 +111,98 @@ def test_counting_leaves_out_bad_entries(pa, kind, H, Hk, D, part, left_over):
         near = np.zeros_like(ref)
         near[:, places[b]] = (p * (2 * 2.0 ** -17 * s + 2.0 ** -20)).sum(1) + (H // Hk + 1) * 2.0 ** -24 * ref[:, places[b]]
         assert np.all(np.abs(w[b] - ref) <= near)  # no tolerance where nothing is added
+
+
+# ---- NaN over cut contexts
+
+
+def _decode(pa, pool, q, t, lens, scale, part, weights=None):
+    """pa_decode or pa_decode_block8, or pa_decode_weights where weights are given."""
+    td, ld, top = dev(t), dev(np.asarray(lens, np.int32)), max(lens)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    out = torch.zeros(q.shape, dtype=pool.dtype, device="cuda")
+    if weights is not None:
+        pa.pa_decode_weights(out, weights, q, pool.k, pool.v, td, ld, top, scale, part, ws, **pool.kw, **pool.one)
+    elif pool.kw:
+        pa.pa_decode_block8(out, q, pool.k, pool.v, pool.kw["k_scales"], pool.kw["v_scales"], td, ld, top, scale, part, ws)
+    else:
+        pa.pa_decode(out, q, pool.k, pool.v, td, ld, top, scale, part, ws, **pool.one)
+    assert pa.pa_get_status() == 0
+    return out
+
+
+@pytest.mark.parametrize("kind", POOLS)
+@pytest.mark.parametrize("counting", [False, True])
+@pytest.mark.parametrize("part", [0, 64, 65536])
+def test_nan_query_gives_nan(pa, kind, counting, part):
+    # One head's query holds a NaN: all its scores are NaN, in every slice that its context is cut into. Its output is
+    # NaN (and so are its KV head's weights), wherever the cuts lie; the other heads' outputs are what they were.
+    rng = np.random.default_rng([63, part])
+    lens, H, Hk, D = [1000, 16, 5], 8, 2, 128
+    nb, t = tables_of(rng, lens)
+    pool = Pool(rng, kind, nb, Hk, D, t, lens)
+    q = torch.from_numpy(rng.standard_normal((3, H, D))).to(pool.dtype)
+    att = R.attend(q.double().numpy(), pool.k64, pool.v64, t, lens, 0.1, host(pool.kw["v_scales"]) if pool.kw else None)
+    tol = bounds(att, torch.finfo(pool.dtype).eps / 2)
+    q[0, 3, 5] = q[1, 0, 0] = float("nan")
+    w = torch.zeros(3, Hk, 1000, device="cuda") if counting else None
+    out = _decode(pa, pool, q.cuda(), t, lens, 0.1, part, w).double().cpu().numpy()
+    hit = np.zeros((3, H), bool)
+    hit[0, 3] = hit[1, 0] = True
+    assert np.all(np.isnan(out[hit]))
+    ref = np.stack([a[0] for a in att])
+    assert np.all(np.abs(out - ref)[~hit] <= tol[~hit])
+    if counting:
+        nan = w.isnan().cpu().numpy()
+        for b, n in enumerate(lens):
+            assert np.array_equal(nan[b, :, :n], np.repeat([[b < 2], [False]], n, 1)) and not nan[b, :, n:].any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "fp8", "e4m3"])
+@pytest.mark.parametrize("part", [0, 64, 65536])
+def test_block_of_nan_keys_gives_nan(pa, kind, part):
+    # A slice of its own may hold nothing but a block of NaN keys; the heads that read it give NaN all the same.
+    rng = np.random.default_rng([64, part])
+    lens, H, Hk, D = [333, 40], 8, 2, 64
+    nb, t = tables_of(rng, lens)
+    pool = Pool(rng, kind, nb, Hk, D, t, lens)
+    q = torch.from_numpy(rng.standard_normal((2, H, D))).to(pool.dtype)
+    att = R.attend(q.double().numpy(), pool.k64, pool.v64, t, lens, 0.1, host(pool.kw["v_scales"]) if pool.kw else None)
+    pool.k[int(t[0, 7]), :, 1] = 0x7F if pool.k.dtype == torch.uint8 else float("nan")
+    out = _decode(pa, pool, q.cuda(), t, lens, 0.1, part).double().cpu().numpy()
+    assert np.all(np.isnan(out[0, 4:]))
+    ref, tol = np.stack([a[0] for a in att]), bounds(att, torch.finfo(pool.dtype).eps / 2)
+    assert np.all(np.abs(out - ref)[0, :4] <= tol[0, :4]) and np.all(np.abs(out - ref)[1] <= tol[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("part", [0, 64, 65536])
+def test_scores_of_minus_infinity(pa, kind, part):
+    # Keys of -inf and positive queries: scores of -inf. A context of nothing else gives zeros and leaves the weights;
+    # among others they count for nothing.
+    rng = np.random.default_rng([65, part])
+    lens, H, Hk, D = [300, 50, 20], 8, 2, 64
+    nb, t = tables_of(rng, lens)
+    pool = Pool(rng, kind, nb, Hk, D, t, lens)
+    q = torch.from_numpy(np.abs(rng.standard_normal((3, H, D))) + 0.01).to(pool.dtype)
+    places = [np.arange(16 * 5, 300), np.arange(0), np.arange(20)]
+    for i in list(range(5)):
+        pool.k[int(t[0, i])] = float("-inf")
+    for i in range(4):
+        pool.k[int(t[1, i])] = float("-inf")
+    rows = np.full_like(t, 0)
+    rows[0, :t.shape[1] - 5], rows[2] = t[0, 5:], t[2]
+    att = R.attend(q.double().numpy(), pool.k64, pool.v64, rows, [220, 0, 20], 0.1, None)
+    tol = bounds(att, torch.finfo(pool.dtype).eps / 2)
+    w = torch.zeros(3, Hk, 300, device="cuda")
+    for weights in (None, w):
+        out = _decode(pa, pool, q.cuda(), t, lens, 0.1, part, weights).double().cpu().numpy()
+        assert np.all(np.abs(out - np.stack([a[0] for a in att])) <= tol)
+    w = w.double().cpu().numpy()
+    for b in range(3):
+        ref = np.zeros((Hk, 300))
+        p, s = (x.reshape(Hk, H // Hk, -1) for x in (att[b][1], att[b][3]))
+        ref[:, places[b]] = p.sum(1)
+        near = np.zeros((Hk, 300))
+        near[:, places[b]] = (p * (2 * 2.0 ** -17 * s + 2.0 ** -20)).sum(1) + (H // Hk + 1) * 2.0 ** -24 * p.sum(1)
+        assert np.all(np.abs(w[b] - ref) <= near)
