@@ -9,7 +9,10 @@
 // fixed point (pa_rope_plan.step), so position * step mod 2^64 is the angle's
 // fraction of a turn for any position: integer wrap-around is the range reduction,
 // exact, where a 32-bit product of a position in the millions would be off by
-// hundredths of a radian. The top 32 bits go through sincospif.
+// hundredths of a radian. The quarter turns come off in integers too, so that what is
+// rounded to fp32 for sincospif is at most an eighth of a turn: off by 2^-24 of itself,
+// at most 2^-28 of a turn, less than the step of an fp32 cosine. (Half a turn would be
+// off by 2^-26 of a turn, more than that step.)
 //
 // Bound by memory: a token moves 2 H D (q) + 4 Hk D (k, v) elements and computes
 // rot_dim / 2 angles, shared by all heads. A CTA takes four tokens (one when there are few,
@@ -123,10 +126,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     for (int i = threadIdx.x; i < count * half; i += kRopeThreads) {
         const int t = i / half, f = i - t * half;
         const uint64_t phase = static_cast<uint64_t>(__ldg(prm.positions + t0 + t)) * prm.plan.step[f];
-        // nearest 32-bit fraction of a turn, as a signed one in half turns
-        const int32_t frac = static_cast<int32_t>((phase + 0x80000000ull) >> 32);
+        // the nearest quarter of a turn, and the signed rest: an eighth of a turn at most, rounded to fp32
+        const int quarter = static_cast<int>((phase + (1ull << 61)) >> 62);
+        const int64_t rest = static_cast<int64_t>(phase - (static_cast<uint64_t>(quarter) << 62));
         float s, c;
-        sincospif(static_cast<float>(frac) * 0x1p-31f, &s, &c);
+        sincospif(static_cast<float>(rest) * 0x1p-63f, &s, &c);
+        if (quarter & 1) {
+            const float x = c;
+            c = -s;
+            s = x;
+        }
+        if (quarter & 2) {
+            c = -c;
+            s = -s;
+        }
         turn[t][f % V * UNITS + f / V] = make_float2(c * prm.plan.mscale, s * prm.plan.mscale);
     }
     if (threadIdx.x < count) {
