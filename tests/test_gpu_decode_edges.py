@@ -206,3 +206,32 @@ def test_scores_of_minus_infinity(pa, kind, part):
         near = np.zeros((Hk, 300))
         near[:, places[b]] = (p * (2 * 2.0 ** -17 * s + 2.0 ** -20)).sum(1) + (H // Hk + 1) * 2.0 ** -24 * p.sum(1)
         assert np.all(np.abs(w[b] - ref) <= near)
+
+
+# ---- how many digits the probabilities keep
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("H,Hk,D", [(32, 8, 128), (64, 8, 128), (4, 2, 64), (3, 3, 128)])
+@pytest.mark.parametrize("counting", [False, True])
+def test_block8_probabilities_keep_their_digits(pa, code, H, Hk, D, counting):
+    # Queries of zero: every probability is 1 / n and no score has an error. The value scales are no powers of two, so
+    # each block's p v_scale is another number, and whatever rounding it meets shows where values cancel.
+    rng = np.random.default_rng([66, H, D])
+    lens = [32] * 24 + [31, 17, 16, 1]
+    nb, t = tables_of(rng, lens)
+    pool = Pool(rng, code, nb, Hk, D, t, lens)
+    vs = np.exp2(rng.random((nb, Hk)) * 2).astype(np.float32)
+    pool.kw["v_scales"] = dev(vs)
+    v64 = R.dequantized(host(pool.v), vs, code)
+    q = torch.zeros(len(lens), H, D, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(len(lens), Hk, 32, device="cuda") if counting else None
+    att = R.attend(q.double().cpu().numpy(), pool.k64, v64, t, lens, 0.1, vs)
+    ref, a = np.stack([x[0] for x in att]), np.stack([x[2] for x in att])
+    # p v_scale = 2^(log2(v_scale) - r): the logarithm to 2^-21, r and the difference rounded to fp32 (numbers below 16:
+    # 2^-21 each), two exponentials to 2^-21, p's two f16 parts 2^-21: less than 2^-18 in all; a few sums in fp32 that
+    # may cut (2^-23 each): 2^-17 covers both.
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -17 * a
+    for part in (0, 64, 65536):
+        got = _decode(pa, pool, q, t, lens, 0.1, part, w).double().cpu().numpy()
+        assert np.all(np.abs(got - ref) <= tol), float((np.abs(got - ref) / (tol + 1e-30)).max())
