@@ -20,6 +20,7 @@ namespace pa {
 enum Block8Format { kBlockE4M3 = 0, kBlockInt8 = 1 };
 
 constexpr int kScaleExpMin = -64, kScaleExpMax = 120;  // 2^e and 2^-e are normal fp32 numbers
+constexpr float kLargestFloat = 3.402823466e38f;
 
 // The least e with amax <= CODE_MAX * 2^e, clamped; amax finite, >= 0.
 // CODE_MAX is 1.75 * 2^8 or 127/128 * 2^7, so e follows from amax's exponent and
@@ -39,7 +40,7 @@ __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static
 // would leave nothing of the block's other rows; an infinity saturates instead).
 __device__ __forceinline__ float finite_abs(float x) {
     const float a = fabsf(x);
-    return a <= 3.402823466e38f ? a : 0.f;
+    return a <= kLargestFloat ? a : 0.f;
 }
 
 // Four fp32 values, already divided by the scale, to four codes (low byte first):

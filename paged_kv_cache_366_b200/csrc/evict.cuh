@@ -292,17 +292,17 @@ __device__ __forceinline__ void widen16(const uint4 &v, uint32_t (&h)[8]) {
     widen4_f16<FMT>(v.w, h[6], h[7]);
 }
 
-// The same through fp32, for any ratio: code * s * inv. Rare, and out of line: its registers
+// The same through fp32, for any finite ratio. Rare, and out of line: its registers
 // would cost the copy a third of its warps.
 template <int FMT>
-__device__ __noinline__ uint4 rescale16_any(uint4 v, float s, float inv) {
+__device__ __noinline__ uint4 rescale16_any(uint4 v, float ratio) {
     uint32_t h[8], w[4];
     widen16<FMT>(v, h);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i]));
         const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i + 1]));
-        w[i] = encode4<FMT>(a.x * s * inv, a.y * s * inv, b.x * s * inv, b.y * s * inv);
+        w[i] = encode4<FMT>(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -351,7 +351,8 @@ __device__ __forceinline__ void copy_rows(unsigned char *pool, float *scales, in
         for (int st = 0; st < STEPS; ++st) {
             uint32_t h[8];
             widen16<FMT>(v[st], h);
-            amax = fmaxf(amax, finite_abs(largest16(h) * s[st]));
+            // a finite code times a finite scale may pass fp32's range (the write makes 256 * 2^120)
+            amax = fmaxf(amax, fminf(largest16(h) * s[st], kLargestFloat));
         }
         const int e = scale_exponent<FMT>(warp_max(amax));
         const float scale = exp2_int(e), inv = exp2_int(-e);
@@ -365,7 +366,8 @@ __device__ __forceinline__ void copy_rows(unsigned char *pool, float *scales, in
                 widen16<FMT>(v[st], h);
                 v[st] = rescale16<FMT>(h, fmaxf(ratio, 0x1p-24f));
             } else {
-                v[st] = rescale16_any<FMT>(v[st], s[st], inv);
+                // an infinite ratio has codes of zero only: the new scale holds every other
+                v[st] = rescale16_any<FMT>(v[st], fminf(ratio, kLargestFloat));
             }
         }
     }
