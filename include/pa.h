@@ -424,8 +424,9 @@ int64_t pa_decode_block8_workspace_bytes(int32_t num_seqs, int32_t max_context_l
  * accumulate in fp32; q enters the products as f16 after division by a power of two for
  * each head, probabilities as two f16 (22 bits) with 2^-32 of the largest as their
  * smallest step.
- * max_context_len and 16 * max_blocks_per_seq up to 2^30 (PA_ERR_UNSUPPORTED beyond), here
- * and in pa_decode_weights and pa_evict.
+ * max_context_len and 16 * max_blocks_per_seq up to 2^30 and num_seqs * Hk below 2^31
+ * (PA_ERR_UNSUPPORTED beyond, from the workspace sizes too), here and in
+ * pa_decode_weights and pa_evict.
  * Several query tokens of one sequence (a verify chunk) are several rows with the same
  * block table and each its own length.
  */
@@ -450,7 +451,8 @@ int pa_decode_block8(void *out, const void *q, const void *k_codes, const void *
  *               (short lists are cut into more slices), then fp32, B * H *
  *               (max_context_len rounded up to 16) scores and B * H sums
  * Each weight is written by one thread, so results repeat bit for bit. Calls that overlap
- * on the GPU must not share a workspace. Three launches.
+ * on the GPU must not share a workspace. Three launches. num_seqs * Hk *
+ * ceil(max_context_len / 1024) must be below 2^31 (PA_ERR_UNSUPPORTED).
  */
 int64_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t max_context_len, int32_t partition_tokens,
                                           const pa_shape *shape);

@@ -135,6 +135,7 @@ int block8_share(const pa_shape *s) { return s->num_kv_heads % 4 == 0 ? 4 : s->n
 int geometry_of(int32_t num_seqs, int32_t max_context_len, int32_t partition_tokens, const pa_shape *s,
                 DecodeGeometry *g) {
     if (max_context_len > kMaxContext) return PA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(num_seqs) * s->num_kv_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     if (!is_block8(s)) {
         DecodeFit fit = decode_fit(s);
         fit.min_blocks = 1;
@@ -160,6 +161,13 @@ struct CountSpace {
     int64_t score_rows, scores_at, lse_at, bytes;
 };
 
+// Whether the counting grid holds every piece of every (sequence, KV head)'s weights; the sizes of a
+// workspace for it then fit 64 bits.
+bool count_fits(int32_t num_seqs, int32_t max_context_len, const pa_shape *s) {
+    return static_cast<int64_t>(num_seqs) * s->num_kv_heads *
+               ((max_context_len + pa::kCountEntries - 1) / pa::kCountEntries) <= 0x7fffffff;
+}
+
 CountSpace count_space(const DecodeGeometry &g, int32_t num_seqs, int32_t max_context_len, const pa_shape *s) {
     CountSpace c;
     c.score_rows = (static_cast<int64_t>(max_context_len) + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE * PA_BLOCK_SIZE;
@@ -180,7 +188,6 @@ int fill_decode(pa::DecodeParams *prm, DecodeGeometry *g, void *out, const void 
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned(block_tables, 4) ||
         !aligned(context_lens, 4))
         return PA_ERR_ALIGNMENT;
-    if (static_cast<int64_t>(num_seqs) * s->num_kv_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     const int rc = geometry_of(num_seqs, max_context_len, partition_tokens, s, g);
     if (rc != PA_OK) return rc;
     if (!workspace) return PA_ERR_WORKSPACE;
@@ -463,7 +470,9 @@ int64_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t max_context_
     if (rc != PA_OK) return rc;
     DecodeGeometry g;
     rc = geometry_of(num_seqs, max_context_len, partition_tokens, shape, &g);
-    return rc == PA_OK ? count_space(g, num_seqs, max_context_len, shape).bytes : rc;
+    if (rc != PA_OK) return rc;
+    if (!count_fits(num_seqs, max_context_len, shape)) return PA_ERR_UNSUPPORTED;
+    return count_space(g, num_seqs, max_context_len, shape).bytes;
 }
 
 int pa_decode_weights(void *out, float *weights, int32_t weights_width, const void *q, const void *k_cache,
@@ -484,13 +493,11 @@ int pa_decode_weights(void *out, float *weights, int32_t weights_width, const vo
     rc = fill_decode(&p.d, &g, out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
                      max_context_len, scale, partition_tokens, workspace, shape);
     if (rc != PA_OK) return rc;
+    if (!count_fits(num_seqs, max_context_len, shape)) return PA_ERR_UNSUPPORTED;
     const CountSpace c = count_space(g, num_seqs, max_context_len, shape);
     if (workspace_bytes < c.bytes) return PA_ERR_WORKSPACE;
     p.d.scores = reinterpret_cast<float *>(static_cast<char *>(workspace) + c.scores_at);
     p.d.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + c.lse_at);
-    if (static_cast<int64_t>(num_seqs) * shape->num_kv_heads *
-            ((max_context_len + pa::kCountEntries - 1) / pa::kCountEntries) > 0x7fffffff)
-        return PA_ERR_UNSUPPORTED;
     p.d.score_rows = static_cast<int>(c.score_rows);
     p.d.weights = weights;
     p.d.weights_width = weights_width;
