@@ -218,6 +218,18 @@ int fill_decode(pa::DecodeParams *prm, DecodeGeometry *g, void *out, const void 
 
 // ---- eviction --------------------------------------------------------------------
 
+// CTAs of a row's selection: as many as bring their share to kSelectShare keys, up to a portable cluster.
+int select_ranks(int32_t max_context_len) {
+    int ranks = 1;
+    while (ranks < pa::kSelectMaxCluster && static_cast<int64_t>(ranks) * pa::kSelectShare < max_context_len) ranks *= 2;
+    return ranks;
+}
+
+// Four warps' pieces each, a KV head, of K and V apart for block8 pools.
+int64_t copy_rows_of_grid(const pa_shape *s) {
+    return (static_cast<int64_t>(s->num_kv_heads) * (is_block8(s) ? 2 : 1) + 3) / 4;
+}
+
 template <int THREADS>
 int launch_evict_select(const pa::EvictParams &p, int64_t units, cudaStream_t st) {
     auto kernel = pa::evict_select_kernel<THREADS>;
@@ -231,11 +243,7 @@ int launch_evict_select(const pa::EvictParams &p, int64_t units, cudaStream_t st
         if (e != cudaSuccess) return cuda_fail(e);
         ready[dev].store(true, std::memory_order_release);
     }
-    // CTAs of a row: as many as bring their share to kSelectShare keys, up to a portable cluster
-    int ranks = 1;
-    while (ranks < pa::kSelectMaxCluster && static_cast<int64_t>(ranks) * pa::kSelectShare < p.max_context_len)
-        ranks *= 2;
-    if (units * ranks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    const int ranks = select_ranks(p.max_context_len);
     const int held = std::min((p.max_context_len + ranks - 1) / ranks, pa::kSelectKeys);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -253,10 +261,7 @@ int launch_evict_select(const pa::EvictParams &p, int64_t units, cudaStream_t st
 }
 
 template <int ROW, int FMT>
-int launch_evict_copy(const pa::EvictParams &p, cudaStream_t st) {
-    const int64_t blocks = static_cast<int64_t>(p.num_seqs) * p.dst_blocks;
-    const int parts = FMT >= 0 ? 2 * p.num_kv_heads : p.num_kv_heads;
-    if (blocks > 0x7fffffff || (parts + 3) / 4 > 65535) return PA_ERR_UNSUPPORTED;
+int launch_evict_copy(const pa::EvictParams &p, unsigned y, cudaStream_t st) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -264,7 +269,7 @@ int launch_evict_copy(const pa::EvictParams &p, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), (parts + 3) / 4);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.dst_blocks, y);
     cfg.blockDim = dim3(128);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, pa::evict_copy_kernel<ROW, FMT>, p);
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
@@ -545,7 +550,11 @@ int pa_evict(void *k_cache, void *v_cache, float *k_scales, float *v_scales, con
         !aligned(dst_block_tables, 4) || !aligned(new_weights, 4) || !aligned(new_context_lens, 4) || !aligned(kept, 4))
         return PA_ERR_ALIGNMENT;
     const int64_t units = static_cast<int64_t>(num_seqs) * shape->num_kv_heads;
-    if (units > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    const int64_t copy_y = copy_rows_of_grid(shape);
+    // both grids, before either is launched
+    if (units * select_ranks(max_context_len) > 0x7fffffff ||
+        static_cast<int64_t>(num_seqs) * dst_blocks_per_seq > 0x7fffffff || copy_y > 65535)
+        return PA_ERR_UNSUPPORTED;
     pa::EvictParams p{};
     p.k_cache = static_cast<unsigned char *>(k_cache);
     p.v_cache = static_cast<unsigned char *>(v_cache);
@@ -576,16 +585,17 @@ int pa_evict(void *k_cache, void *v_cache, float *k_scales, float *v_scales, con
                                                               : launch_evict_select<512>(p, units, st);
     if (rc != PA_OK) return rc;
     const int row = shape->head_dim * cache_bytes(shape);
+    const unsigned y = static_cast<unsigned>(copy_y);
     if (is_block8(shape)) {
         if (shape->kv_fp8 == PA_KV_BLOCK_E4M3)
-            return row == 128 ? launch_evict_copy<128, pa::kBlockE4M3>(p, st) : launch_evict_copy<64, pa::kBlockE4M3>(p, st);
-        return row == 128 ? launch_evict_copy<128, pa::kBlockInt8>(p, st) : launch_evict_copy<64, pa::kBlockInt8>(p, st);
+            return row == 128 ? launch_evict_copy<128, pa::kBlockE4M3>(p, y, st) : launch_evict_copy<64, pa::kBlockE4M3>(p, y, st);
+        return row == 128 ? launch_evict_copy<128, pa::kBlockInt8>(p, y, st) : launch_evict_copy<64, pa::kBlockInt8>(p, y, st);
     }
     switch (row) {
-        case 64: return launch_evict_copy<64, -1>(p, st);
-        case 128: return launch_evict_copy<128, -1>(p, st);
-        case 256: return launch_evict_copy<256, -1>(p, st);
-        default: return launch_evict_copy<512, -1>(p, st);
+        case 64: return launch_evict_copy<64, -1>(p, y, st);
+        case 128: return launch_evict_copy<128, -1>(p, y, st);
+        case 256: return launch_evict_copy<256, -1>(p, y, st);
+        default: return launch_evict_copy<512, -1>(p, y, st);
     }
 }
 

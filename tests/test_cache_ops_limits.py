@@ -3,7 +3,7 @@ call and by the function that sizes its workspace. Pointers are made up; every r
 them."""
 import pytest
 
-from test_cache_ops_host import by, decode_args, lib, shape
+from test_cache_ops_host import by, decode_args, evict_args, lib, shape
 from test_cache_ops_host import J_ as WEIGHTS
 
 UNSUPPORTED = -2
@@ -41,3 +41,13 @@ def test_largest_sizes_have_a_workspace():
             n = lib().pa_decode_weights_workspace_bytes(B, top, 0, by(s))
             assert n > B * 32 * top * 4  # the scores alone
     assert lib().pa_decode_block8_workspace_bytes((1 << 28) - 1, 1 << 30, 0, by(shape(kv_fp8=2))) > 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=1 << 15, db=(1 << 16) + 1, top=16, keep=16), dict(B=1 << 28, db=8, top=16, keep=16),
+    dict(B=1 << 26, top=1 << 20, width=1 << 20, keep=16, db=1),
+    dict(B=1, shape=shape(num_heads=262141, num_kv_heads=262141)),
+])
+def test_evict_refuses_before_its_first_launch(kw):
+    # Without a GPU the first launch gives another error.
+    assert lib().pa_evict(*evict_args(**dict(dict(sinks=0, recent=0), **kw))) == UNSUPPORTED
