@@ -83,3 +83,59 @@ def test_any_finite_scales(pa, monkeypatch, code):
 
     monkeypatch.setattr(E, "Pool", Few)
     check_evict(pa, np.random.default_rng(82), code, [300, 16, 17, 200], 2, 64, 60, 2, 4)
+
+
+# ---- the selection's two sizes: 256 threads where a batch of short rows fills the GPU, else 512 and clusters
+
+
+RAGGED = [0, 1, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 400, 511, 512, 513, 600, 700, 777, 800,
+          900, 1000, 1023, 1024, 1025, 1200, 1500, 1535, 1536, 1537, 1800, 2000, 2046, 2047, 2048]
+
+
+@pytest.mark.parametrize("keep,sinks,recent", [(1, 0, 0), (256, 4, 128), (300, 0, 0), (1025, 0, 1025), (2047, 4, 32)])
+def test_many_short_rows(pa, keep, sinks, recent):
+    # 39 sequences of 8 heads are more rows than SMs
+    check_evict(pa, np.random.default_rng([91, keep]), "bf16", RAGGED, 8, 64, keep, sinks, recent)
+
+
+@pytest.mark.parametrize("kind", ["f32", "fp8", "e4m3", "int8"])
+def test_many_short_rows_of_every_pool(pa, kind):
+    check_evict(pa, np.random.default_rng(92), kind, RAGGED, 8, 64, 256, 4, 128)
+
+
+@pytest.mark.parametrize("top", [2048, 2049, 40000])
+def test_many_rows_around_the_border(pa, top):
+    # the same rows with a host bound at the border, past it and far past it: both sizes, with and without clusters
+    check_evict(pa, np.random.default_rng(93), "bf16", RAGGED, 8, 64, 100, 4, 10, top=top)
+
+
+def test_many_short_rows_ties_and_odd_weights(pa):
+    rng = np.random.default_rng(94)
+    shape = (len(RAGGED), 8, 2048)
+    for fill in (0.0, 1.0, float("nan"), float("inf"), float("-inf")):
+        check_evict(pa, rng, "bf16", RAGGED, 8, 64, 260, 3, 5, np.full(shape, fill, np.float32))
+    w = rng.integers(0, 3, shape).astype(np.float32)  # many equal weights, cut among them
+    check_evict(pa, rng, "bf16", RAGGED, 8, 64, 250, 0, 0, w)
+    # equal but for the last bits: the digits decide in their last round
+    w = (0x3F800000 + rng.integers(0, 64, shape)).astype(np.uint32).view(np.float32)
+    check_evict(pa, rng, "bf16", RAGGED, 8, 64, 500, 1, 2, w)
+    w = rng.standard_normal(shape).astype(np.float32)
+    w[rng.random(shape) < 0.3] = np.nan
+    w[rng.random(shape) < 0.1] = -0.0
+    w[rng.random(shape) < 0.1] = 0.0
+    w[rng.random(shape) < 0.05] = np.inf
+    w[rng.random(shape) < 0.05] = -np.inf
+    w[rng.random(shape) < 0.05] = 1e-42
+    check_evict(pa, rng, "bf16", RAGGED, 8, 64, 400, 10, 20, w)
+
+
+# ---- counting for more sequences than the merge scans
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3", "int8"])
+@pytest.mark.parametrize("part", [0, 64])
+def test_counting_many_sequences(pa, kind, part):
+    # more than 256: the merge before the counting takes its slices from the records that the decode kernel leaves
+    rng = np.random.default_rng([95, part])
+    lens = [int(n) for n in rng.integers(0, 90, 299)] + [1500]
+    E.check_count(pa, rng, kind, lens, 8, 2, 64, part=part, steps=2)
