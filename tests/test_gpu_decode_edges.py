@@ -235,3 +235,57 @@ def test_block8_probabilities_keep_their_digits(pa, code, H, Hk, D, counting):
     for part in (0, 64, 65536):
         got = _decode(pa, pool, q, t, lens, 0.1, part, w).double().cpu().numpy()
         assert np.all(np.abs(got - ref) <= tol), float((np.abs(got - ref) / (tol + 1e-30)).max())
+
+
+# ---- the ends of the scales' range
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("H,Hk,D", [(16, 4, 128), (64, 8, 64), (2, 2, 128)])
+@pytest.mark.parametrize("part", [0, 64, 65536])
+@pytest.mark.parametrize("counting", [False, True])
+def test_value_scales_over_their_whole_range(pa, code, H, Hk, D, part, counting):
+    # The write makes scales from 2^-64 to 2^120. Sequences of scales near either end, of all sizes mixed, and of scales
+    # below the write's that a caller may have; sums of 2^100 * 448 * 400 are still bf16 numbers.
+    rng = np.random.default_rng([67, H, D, part])
+    lens = [400, 399, 17, 100, 33, 1]
+    ends = [(-64, -60), (96, 100), (-64, 100), (-64, 100), (-100, -90), (100, 100)]
+    nb, t = tables_of(rng, lens)
+    pool = Pool(rng, code, nb, Hk, D, t, lens)
+    vs = host(pool.kw["v_scales"]).copy()
+    for b, (lo, hi) in enumerate(ends):
+        at = t[b, :R.blocks(lens[b])]
+        vs[at] = np.exp2(rng.integers(lo, hi + 1, (len(at), Hk)))
+    pool.kw["v_scales"] = dev(vs)
+    v64 = R.dequantized(host(pool.v), vs, code)
+    q = bf16(rng.standard_normal((len(lens), H, D)))
+    w = torch.zeros(len(lens), Hk, 400, device="cuda") if counting else None
+    got = _decode(pa, pool, q.cuda(), t, lens, 0.1, part, w).double().cpu().numpy()
+    att = R.attend(q.double().numpy(), pool.k64, v64, t, lens, 0.1, vs)
+    ref, tol = np.stack([x[0] for x in att]), bounds(att, 2.0 ** -8)
+    assert np.all(np.isfinite(got)) and np.all(np.abs(got - ref) <= tol)
+    if counting:
+        for b, n in enumerate(lens):
+            p = att[b][1].reshape(Hk, H // Hk, n)
+            s = att[b][3].reshape(Hk, H // Hk, 1)
+            near = (p * (2 * 2.0 ** -17 * s + 2.0 ** -20)).sum(1) + (H // Hk + 1) * 2.0 ** -24 * p.sum(1)
+            assert np.all(np.abs(w[b, :, :n].double().cpu().numpy() - p.sum(1)) <= near)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_key_scales_over_their_whole_range(pa, code):
+    # Key scales from far below to 2^120, undone by the softmax scale: a sequence of one size each.
+    rng = np.random.default_rng(68)
+    H, Hk, D = 16, 4, 64
+    for e in (-64, -20, 60, 100, 120):
+        lens = [77, 300, 16]
+        nb, t = tables_of(rng, lens)
+        pool = Pool(rng, code, nb, Hk, D, t, lens)
+        ks = np.full((nb, Hk), 2.0 ** e, np.float32)
+        pool.kw["k_scales"] = dev(ks)
+        q = bf16(rng.standard_normal((3, H, D)) * 2.0 ** -6)
+        scale = 0.01 * 2.0 ** -e
+        got = _decode(pa, pool, q.cuda(), t, lens, scale, 0).double().cpu().numpy()
+        att = R.attend(q.double().numpy(), R.dequantized(host(pool.k), ks, code), pool.v64, t, lens, scale,
+                       host(pool.kw["v_scales"]))
+        assert np.all(np.abs(got - np.stack([x[0] for x in att])) <= bounds(att, 2.0 ** -8))
