@@ -578,11 +578,15 @@ int pa_evict(void *k_cache, void *v_cache, float *k_scales, float *v_scales, con
     p.recent = recent;
     p.max_context_len = max_context_len;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // 256 threads for rows of up to 2048 weights, when there are enough to fill the SMs: 64 sequences
-    // of 128 to 2048 entries 54.2 us in all against 55.9, 256 of 100 entries 34.0 against 44.0; but
-    // one sequence of 1500 10.4 against 9.2
-    rc = max_context_len <= 2048 && units >= sms_or_default() ? launch_evict_select<256>(p, units, st)
-                                                              : launch_evict_select<512>(p, units, st);
+    // 256 threads where three CTAs an SM or more wait for one another's barriers, fewer where rows are short
+    // (a thread's keys are few then). The whole call, 512 against 256 threads: 800 rows of up to 1024 entries 37.3
+    // and 33.5 us, 128 rows 11.1 and 11.8; 448 rows of up to 2048 37.0 and 35.6, 208 rows 21.9 and 22.1; 800 rows
+    // of up to 4096 106 and 103, 352 rows 50.5 and 52.0; 72 rows of up to 32768 (576 CTAs) 87.8 and 81.3, 24 rows
+    // 38.1 and 40.6 (bf16, rows of 64, a quarter kept).
+    const int64_t ctas = units * select_ranks(max_context_len);
+    rc = ctas >= static_cast<int64_t>(sms_or_default()) * std::min(3, (max_context_len + 1023) / 1024)
+             ? launch_evict_select<256>(p, units, st)
+             : launch_evict_select<512>(p, units, st);
     if (rc != PA_OK) return rc;
     const int row = shape->head_dim * cache_bytes(shape);
     const unsigned y = static_cast<unsigned>(copy_y);

@@ -78,9 +78,9 @@ __device__ __forceinline__ int scan_before(int v, int *warp_sums, int &all) {
     return inc - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
 }
 
-// THREADS: 512, digits of 9 + 9 + 9 + 5 bits, or 256, four of 8. 2048 threads an SM: a CTA mostly waits (for loads, shared-memory
-// atomics, barriers), and the rows of a batch of 64 sequences with 8 KV heads then fit the
-// GPU at once.
+// THREADS: 512, digits of 9 + 9 + 9 + 5 bits, or 256, four of 8. 2048 threads an SM: a CTA
+// mostly waits (for loads, shared-memory atomics, barriers), and the rows of a batch of 64
+// sequences with 8 KV heads then fit the GPU at once.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(const EvictParams prm, int keys_held) {
     extern __shared__ __align__(16) uint32_t select_keys[];

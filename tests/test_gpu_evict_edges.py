@@ -85,7 +85,7 @@ def test_any_finite_scales(pa, monkeypatch, code):
     check_evict(pa, np.random.default_rng(82), code, [300, 16, 17, 200], 2, 64, 60, 2, 4)
 
 
-# ---- the selection's two sizes: 256 threads where a batch of short rows fills the GPU, else 512 and clusters
+# ---- the selection's two sizes: 256 threads where many rows fill the GPU, else 512, each with clusters for long rows
 
 
 RAGGED = [0, 1, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 400, 511, 512, 513, 600, 700, 777, 800,
@@ -107,6 +107,11 @@ def test_many_short_rows_of_every_pool(pa, kind):
 def test_many_rows_around_the_border(pa, top):
     # the same rows with a host bound at the border, past it and far past it: both sizes, with and without clusters
     check_evict(pa, np.random.default_rng(93), "bf16", RAGGED, 8, 64, 100, 4, 10, top=top)
+
+
+def test_many_rows_one_too_long_for_shared_memory(pa):
+    # 56 rows of a host bound that takes clusters of eight; one row is longer than they hold
+    check_evict(pa, np.random.default_rng(96), "fp8", [430000, 70] + RAGGED + [5] * 15, 1, 64, 777, 4, 500)
 
 
 def test_many_short_rows_ties_and_odd_weights(pa):
