@@ -344,7 +344,8 @@ typedef struct {
  * pa_rope_init: fill a plan. rot_dim is a multiple of 16, 16 .. 128 (else
  * PA_ERR_UNSUPPORTED); base >= 1; factor >= 1 unless scaling is PA_ROPE_NONE; low,
  * high and original_len count for PA_ROPE_PARTS only (0 <= low < high,
- * original_len > 0). mscale multiplies cos and sin (1 for none). Host only.
+ * original_len > 0). mscale multiplies cos and sin (1 for none) and is finite
+ * in fp32. Host only.
  */
 int pa_rope_init(pa_rope_plan *plan, int32_t rot_dim, int32_t interleaved, double base, int32_t scaling, double factor,
                  double low, double high, double original_len, double mscale);

@@ -283,7 +283,7 @@ int pa_rope_init(pa_rope_plan *plan, int32_t rot_dim, int32_t interleaved, doubl
                  double low, double high, double original_len, double mscale) {
     if (!plan || (interleaved != 0 && interleaved != 1)) return PA_ERR_INVALID_ARGUMENT;
     if (rot_dim < 16 || rot_dim > PA_ROPE_MAX_DIM || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
-    if (!std::isfinite(base) || base < 1.0 || !std::isfinite(mscale)) return PA_ERR_INVALID_ARGUMENT;
+    if (!std::isfinite(base) || base < 1.0 || !std::isfinite(static_cast<float>(mscale))) return PA_ERR_INVALID_ARGUMENT;
     if (scaling < PA_ROPE_NONE || scaling > PA_ROPE_PARTS) return PA_ERR_INVALID_ARGUMENT;
     if (scaling != PA_ROPE_NONE && !(std::isfinite(factor) && factor >= 1.0)) return PA_ERR_INVALID_ARGUMENT;
     if (scaling == PA_ROPE_PARTS &&

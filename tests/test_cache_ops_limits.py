@@ -51,3 +51,12 @@ def test_largest_sizes_have_a_workspace():
 def test_evict_refuses_before_its_first_launch(kw):
     # Without a GPU the first launch gives another error.
     assert lib().pa_evict(*evict_args(**dict(dict(sinks=0, recent=0), **kw))) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("mscale", [1e39, -1e39, 3.4028236e38])
+def test_rope_plan_refuses_a_factor_past_fp32(mscale):
+    # the plan holds it in fp32, and the rotary calls refuse an infinite one
+    from paged_kv_cache_366_b200 import pa
+    plan = pa.PaRopePlan()
+    assert lib().pa_rope_init(by(plan), 64, 0, 1e4, 0, 1.0, 1.0, 32.0, 0.0, mscale) == -1
+    assert lib().pa_rope_init(by(plan), 64, 0, 1e4, 0, 1.0, 1.0, 32.0, 0.0, 3.4e38) == 0
