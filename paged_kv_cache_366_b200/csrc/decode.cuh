@@ -903,6 +903,7 @@ __global__ void __launch_bounds__(32 * MG) decode_merge_kernel(const DecodeParam
         Lsum *= a;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            if (p0 + i * MG >= nseg) break;
             const float wt = mp[i] == mc ? 1.f : exp2f(mp[i] - mc);
             O.x += wt * op[i].x;
             O.y += wt * op[i].y;
