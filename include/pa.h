@@ -423,8 +423,8 @@ int64_t pa_decode_block8_workspace_bytes(int32_t num_seqs, int32_t max_context_l
  * pa_decode, with the scales ([NB][Hk] each, any finite values >= 0); like it, calls that
  * overlap on the GPU must not share a workspace. Scores, softmax sums and outputs
  * accumulate in fp32; q enters the products as f16 after division by a power of two for
- * each head, probabilities as two f16 (22 bits) with 2^-32 of the largest as their
- * smallest step.
+ * each head (exact down to 2^-17 of the head's largest), probabilities as two f16
+ * (22 bits) with 2^-32 of the largest as their smallest step.
  * max_context_len and 16 * max_blocks_per_seq up to 2^30 and num_seqs * Hk below 2^31
  * (PA_ERR_UNSUPPORTED beyond, from the workspace sizes too), here and in
  * pa_decode_weights and pa_evict.

@@ -12,8 +12,8 @@
 // Sharing one launch with the merge, each counting CTA summing its unit's partial
 // denominators itself, was slower (decode batch 64.3 us against 58.3): that sum is a chain
 // of loads in every CTA. Here the scores, the weights and the denominators are loaded at
-// once. Counting adds 8 us to the decode batch over bf16 (48 to 56 us) and 17 us to 64
-// contexts of 4096 tokens over E4M3 (96 to 113): bound by launch latency there, and here by
+// once. Counting adds 8 us to the decode batch over bf16 (48 to 56 us) and 20 us to 64
+// contexts of 4096 tokens over E4M3 (88 to 108): bound by launch latency there, and here by
 // the scores' way through L2 and back.
 #pragma once
 

@@ -12,16 +12,16 @@
 //
 // Producer warps walk the slices and issue every load, a lane a slice; the consumer warps
 // only compute. Four of them: one lane's loads hold up its warp's others, and a single
-// producer took 95.5 us for eight 32 K contexts where four take 87.6, and 77.8 instead of
-// 52.5 us with one KV head (twelve slices to serve). At the copy bandwidth an SM has about 180 cycles for a block of one
-// KV head, half of a bf16 cache's, and the packed-FMA step of decode_kernel takes over 750
-// issue slots. So the block step is two small matrix products on the warp's tensor
-// instructions (m16n8k16, f16 operands, fp32 sums), about 300 issue slots in all for E4M3
-// and 400 for INT8:
+// producer took 95.5 us for eight 32 K contexts where four took 87.6, and 77.8 instead of
+// 52.5 us with one KV head (twelve slices to serve). At the copy bandwidth an SM has about
+// 180 cycles for a block of one KV head, half of a bf16 cache's, and the packed-FMA step of
+// decode_kernel takes over 750 issue slots. So the block step is two small matrix products
+// on the warp's tensor instructions (m16n8k16, f16 operands, fp32 sums), about 300 issue
+// slots in all for E4M3 and 400 for INT8:
 //  * S^T[16 tokens][8 heads] = K Q^T. K's codes widen exactly to f16 in registers; the
-//    group's heads fill the 8 columns (the rest are 0). tcgen05 wants 64 or more rows of
-//    a product at once and the operands in shared memory; widening through shared memory
-//    would cost more than these 16 instructions do.
+//    group's heads fill the 8 columns, up to four of them twice (below). tcgen05 wants 64
+//    or more rows of a product at once and the operands in shared memory; widening through
+//    shared memory would cost more than these 16 instructions do.
 //  * O^T[D][8 heads] += V^T P. The block's probabilities go from the first product's
 //    accumulator layout to the second's operand layout by a register transpose
 //    (movmatrix), and V's codes of two tokens are paired byte by byte before widening.
@@ -30,7 +30,8 @@
 // are ordered (kTau) so that those reads of TMA-swizzled rows meet no bank conflict.
 //
 // Numbers. Scores, maxima, sums and O are fp32. q enters as f16 after division by its
-// head's power of two (so a bf16 value is exact down to 2^-22 of the head's largest);
+// head's power of two: a bf16 value is exact down to 2^-17 of that power (its 8 bits then
+// end at f16's smallest step, 2^-24), and off by at most 2^-25 of it below.
 // p enters P V as two f16, its first 11 bits and the next 11. Up to four heads leave half
 // of the product's columns free: head g's first part is column g, its second column 4 + g
 // (whose scores come from the same queries once more), and a close adds the two, so the
@@ -44,9 +45,12 @@
 // must not vanish). The softmax sum uses 2^(s - m). A close multiplies O by 2^(r - m).
 //
 // Measured (32/8 heads of 128): 64 sequences of 128 to 2048 tokens over E4M3 32.7 us, 0.65
-// of the measured copy bandwidth, of which about 10 us are the start (lengths, tables, first
-// loads) and the merge; eight of 32 K tokens over INT8 87.6 us, 0.94 (100 us where the
-// 1000 W power cap holds the clock at 1.6 GHz: INT8's conversions then bound it).
+// of the measured copy bandwidth. By time stamps the first blocks have landed after 5 us
+// (lengths, their scan, tables, first loads), the median slice ends 5 us before the last
+// (equal blocks are not equal time where a slice crosses several short contexts), and the
+// merge with its launch takes 3.5. Eight of 32 K tokens over INT8: 103 us, 0.80, in calls
+// that follow one another for long, where the 1000 W power cap holds the clock at 1.6 GHz
+// and INT8's conversions bound it; 87.5 us, 0.94, in short runs at 1965 MHz.
 #pragma once
 
 #include "block8.cuh"

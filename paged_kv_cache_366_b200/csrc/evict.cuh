@@ -54,8 +54,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // of 64 rows of up to 32 K weights 109 us; one CTA a row took 42.) Bound by latency: up
 // to four rounds of histogram, barrier and scan over a few thousand keys a CTA, which stay
 // in shared memory, so that HBM sees the weights once. 64 sequences of 128 to 2048 entries
-// with 8 KV heads: 14.1 us under ncu (512 threads and three rounds of 2048 bins: 15.1);
-// eight of 9 to 32 K: 28.4.
+// with 8 KV heads: 14 to 15 us under ncu (512 threads and three rounds of 2048 bins were a
+// microsecond slower); eight of 9 to 32 K: 27 to 28.
 constexpr int kSelectShare = 4096;          // keys of a CTA, while 8 CTAs are enough for that
 constexpr int kSelectKeys = 50 * 1024;      // keys a CTA's shared memory holds at most
 constexpr int kSelectMaxCluster = 8;        // the portable cluster size
@@ -246,8 +246,9 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(c
 // so that they are in flight together. (A persistent grid whose warps look up their next
 // piece while they copy took longer, 48 against 39 us for the batch: the registers of the
 // look-ahead cost more warps than it hides.) Measured: a bf16 batch of 64 sequences cut to 512
-// entries, 249 MB, 37 us (6.7 TB/s); eight E4M3 contexts cut to 8191, 128-byte rows from
-// anywhere, 270 MB, 57 us (4.7 TB/s).
+// entries, 249 MB, 37 to 39 us (6.4 to 6.7 TB/s); eight E4M3 contexts cut to 8191, 270 MB, 57
+// to 60 us (4.5 to 4.7 TB/s). On one box 60 us, 58 with scales that need no re-coding, 54
+// where neighbouring rows are kept, and 54 with both: neither is most of what it lacks.
 //
 // FMT >= 0 (block8): a new block's rows come from blocks of different scales; the new
 // scale is the least power of two for its rows' largest magnitude, and the codes are
