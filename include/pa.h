@@ -359,7 +359,7 @@ int pa_rope_init(pa_rope_plan *plan, int32_t rot_dim, int32_t interleaved, doubl
  *   q_out     : [T][H][D]; k_out : [T][Hk][D]. May be q and k themselves where those
  *               are contiguous; must not overlap them otherwise.
  *   positions : int64 [T] device. Whole and quarter turns come off exactly (the turn
- *               is kept in 64-bit fixed point, good to 2^-34 of a turn for
+ *               is kept in 64-bit fixed point, good to 2^-33 of a turn for
  *               |position| < 2^31); the rest, an eighth of a turn at most, is
  *               rounded to fp32: within 2^-28 of a turn.
  * The rotation is fp32, rounded once. The pool fields of `shape` are checked but not
